@@ -31,6 +31,8 @@ EXPORTED = [
     "hkv_store_prefetch", "hkv_store_residency", "hkv_select_pages_policy", "hkv_page_scores", "hkv_select_top",
     "hsa_sparse_attn_lse", "hsa_fidelity", "hkv_page_block_sums", "hkv_block_means_from_pages",
     "hsa_forward_selected", "hsa_forward_ex", "hkv_gather_project", "hsa_inject_fault",
+    "hsa_rope_freqs", "hsa_rope", "hsa_rope_bwd", "hkv_quant_page_size", "hkv_quant_rows", "hkv_gather_quant",
+    "hkv_attn_quant_workspace_size", "hkv_attn_quant",
 ]
 
 FWD_SELECTED, FWD_HISTORY = 1, 2
@@ -65,6 +67,21 @@ class _Selection(ctypes.Structure):
                 ("intra_idx", ctypes.c_void_p), ("intra_cnt", ctypes.c_void_p)]
 
 
+class _Rope(ctypes.Structure):
+    _fields_ = [("layout", ctypes.c_int), ("rot_dim", ctypes.c_int), ("n_axes", ctypes.c_int),
+                ("axis_pairs", ctypes.c_int * 3), ("mscale", ctypes.c_float), ("inv_freq", ctypes.c_void_p)]
+
+
+class _Rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("H", ctypes.c_int), ("token_stride", ctypes.c_longlong),
+                ("head_stride", ctypes.c_longlong)]
+
+
+class Quant(ctypes.Structure):
+    """hkv_quant_t: the format of quantised pages and the columns a scale covers."""
+    _fields_ = [("format", ctypes.c_int), ("group", ctypes.c_int)]
+
+
 _lib = None
 
 
@@ -78,6 +95,7 @@ def load_library(path: str = LIB_PATH):
     lib = ctypes.CDLL(path)
     P, I, L, S, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_size_t, ctypes.c_float
     CP = ctypes.POINTER(Config)
+    RP, XP, QP = ctypes.POINTER(_Rope), ctypes.POINTER(_Rows), ctypes.POINTER(Quant)
     sig = {
         "hsa_status_string": (ctypes.c_char_p, [I]),
         "hsa_last_error_detail": (ctypes.c_char_p, []),
@@ -121,6 +139,14 @@ def load_library(path: str = LIB_PATH):
         "hsa_selftest_wait": (I, [P, P, P]),
         "hsa_thread_release": (I, []),
         "hsa_inject_fault": (I, [I]),
+        "hsa_rope_freqs": (I, [I, ctypes.c_double, I, ctypes.c_double, I, P, ctypes.POINTER(F)]),
+        "hsa_rope": (I, [RP, P, L, I, I, I, XP, XP, XP, XP, P]),
+        "hsa_rope_bwd": (I, [RP, P, L, I, I, I, XP, XP, XP, XP, P]),
+        "hkv_quant_page_size": (I, [QP, I, I, I, ctypes.POINTER(S), ctypes.POINTER(S)]),
+        "hkv_quant_rows": (I, [QP, XP, XP, I, I, I, RP, P, L, P, P, I, I, L, P, P, S, P]),
+        "hkv_gather_quant": (I, [QP, P, P, I, P, I, I, I, I, RP, P, L, P, P, P, P, S, P]),
+        "hkv_attn_quant_workspace_size": (I, [I, I, I, I, I, I, ctypes.POINTER(S)]),
+        "hkv_attn_quant": (I, [QP, P, I, I, P, P, I, P, I, I, I, I, P, F, P, I, P, P, S, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -414,6 +440,212 @@ def hsa_forward_reuse(cfg, Q, Kc, Vc, Kq, Vq, tau, gate_logit, E, F, out, ws, kb
                                             _p(tau), _p(gate_logit), _p(E), _p(F), ef_head_stride, _p(out),
                                             1 if out.dtype == torch.bfloat16 else 0, csel, _p(ws), ws.numel(),
                                             _stream(stream)), "hsa_forward_reuse")
+
+
+# ---------------------------------------------------------------- rotary positions, quantised pages
+
+DTYPE_BF16, DTYPE_FP16, DTYPE_FP32 = 0, 1, 2
+_DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_FP16, torch.float32: DTYPE_FP32}
+ROPE_INTERLEAVED, ROPE_HALF = 0, 1
+ROPE_SCALE_NONE, ROPE_SCALE_LINEAR, ROPE_SCALE_NTK, ROPE_SCALE_YARN = 0, 1, 2, 3
+QUANT_E4M3, QUANT_INT8, QUANT_INT4 = 0, 1, 2
+
+
+def _refuse(where, detail):
+    raise HsaError(1, where, detail)
+
+
+def _tensor(t, what, where, device, dtype, shape=None):
+    """A dense device tensor of `dtype` (and `shape`): its address."""
+    if t.device != device:
+        _refuse(where, f"{what} is on {t.device}, not on {device}")
+    if t.dtype != dtype:
+        _refuse(where, f"{what} is {t.dtype}, not {dtype}")
+    if shape is not None and t.shape != shape:
+        _refuse(where, f"{what} is {list(t.shape)}, not {list(shape)}")
+    if not t.is_contiguous():
+        _refuse(where, f"{what} is not contiguous")
+    return t.data_ptr()
+
+
+def _rows(t, what, where, device, dtype, T, d):
+    """Token rows [T, H, d] whose columns are dense, as an hsa_rows_t."""
+    if t.device != device:
+        _refuse(where, f"{what} is on {t.device}, not on {device}")
+    if t.dtype != dtype:
+        _refuse(where, f"{what} is {t.dtype}, not {dtype}")
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != T or shape[2] != d:
+        _refuse(where, f"{what} is {list(shape)}, not [{T}, heads, {d}]")
+    step, head, column = t.stride()
+    if column != 1:
+        _refuse(where, f"the columns of {what} are not contiguous (stride {column})")
+    if shape[1] == 1:  # torch gives a dimension of one element any stride
+        head = d
+    if T == 1:
+        step = shape[1] * head
+    return _Rows(t.data_ptr(), shape[1], step, head)
+
+
+def _on_device(device, call):
+    """call() with `device` current (the launch goes to the tensors' device)."""
+    if device.type != "cuda":
+        raise HsaError(1, "device", f"the tensors are on {device}, not on a CUDA device")
+    if device.index == torch.cuda.current_device():
+        return call()
+    with torch.cuda.device(device):
+        return call()
+
+
+class Rope:
+    """hsa_rope_t with the table it points at (make_rope)."""
+
+    def __init__(self, inv_freq, layout, axis_pairs, mscale):
+        self.inv_freq, self.device, self.n_axes = inv_freq, inv_freq.device, len(axis_pairs)
+        self.c = _Rope(layout, 2 * inv_freq.numel(), self.n_axes, (ctypes.c_int * 3)(*axis_pairs), mscale, inv_freq.data_ptr())
+
+
+def rope_freqs(dim, base=10000.0, scaling=ROPE_SCALE_NONE, factor=1.0, orig_context=0):
+    """(inv_freq: float64 [dim / 2] on the CPU, mscale) of one axis of `dim` rotated columns."""
+    out = torch.empty(max(dim, 0) // 2, dtype=torch.float64)
+    m = ctypes.c_float(0)
+    _check(load_library().hsa_rope_freqs(dim, base, scaling, factor, orig_context, ctypes.c_void_p(out.data_ptr()),
+                                         ctypes.byref(m)), "hsa_rope_freqs")
+    return out, m.value
+
+
+def make_rope(inv_freq, layout=ROPE_INTERLEAVED, axis_pairs=None, mscale=1.0) -> Rope:
+    """Rotary positions of the first 2 * len(inv_freq) columns.  inv_freq: float64 device tensor, the axes'
+    frequencies one after the other; axis_pairs: how many belong to each axis (default: one axis)."""
+    pairs = [inv_freq.numel()] if axis_pairs is None else [int(n) for n in axis_pairs]
+    if inv_freq.dim() != 1 or not 1 <= len(pairs) <= 3 or sum(pairs) != inv_freq.numel() or min(pairs) < 0:
+        _refuse("make_rope", f"inv_freq {list(inv_freq.shape)} for the axes' pairs {pairs}")
+    _tensor(inv_freq, "inv_freq", "make_rope", inv_freq.device, torch.float64)
+    return Rope(inv_freq, layout, pairs, mscale)
+
+
+def _positions(rope, pos, where, device, tokens):
+    """(rope struct, pos address, row stride) of an optional rotation of `tokens` rows."""
+    if rope is None:
+        if pos is not None:
+            _refuse(where, "pos without rope")
+        return None, None, 0
+    if pos is None:
+        _refuse(where, "rope without pos")
+    if rope.device != device:
+        _refuse(where, f"inv_freq is on {rope.device}, not on {device}")
+    want = (rope.n_axes, tokens)
+    if pos.shape != want and (rope.n_axes != 1 or pos.shape != (tokens,)):
+        _refuse(where, f"pos is {list(pos.shape)}, not {list(want)}")
+    return ctypes.byref(rope.c), _tensor(pos, "pos", where, device, torch.int32), tokens
+
+
+def _rope_call(name, rope, pos, q, q_out, k, k_out, stream):
+    device, dtype = q.device, q.dtype
+    if q.dim() != 3 or dtype not in _DTYPES:
+        _refuse(name, f"q is {list(q.shape)} {dtype}: [T, heads, d] bfloat16, float16 or float32 wanted")
+    T, _, d = q.shape
+    qi, qo = _rows(q, "q", name, device, dtype, T, d), _rows(q_out, "q_out", name, device, dtype, T, d)
+    ki = ko = None
+    if (k is None) != (k_out is None):
+        _refuse(name, "k and k_out go together")
+    if k is not None:
+        ki = ctypes.byref(_rows(k, "k", name, device, dtype, T, d))
+        ko = ctypes.byref(_rows(k_out, "k_out", name, device, dtype, T, d))
+    r, at, step = _positions(rope, pos, name, device, T)
+    fn = getattr(load_library(), name)
+    _on_device(device, lambda: _check(fn(r, at, step, T, d, _DTYPES[dtype], ctypes.byref(qi), ctypes.byref(qo), ki, ko,
+                                         _stream(stream)), name))
+
+
+def hsa_rope(rope, pos, q, q_out, k=None, k_out=None, stream=None):
+    """Rotate queries [T, Hq, d] and keys [T, Hk, d] by their positions (int32 [n_axes, T], or [T] for one axis).
+    Rows may be strided (heads of a fused projection); q_out may be q, k_out may be k."""
+    _rope_call("hsa_rope", rope, pos, q, q_out, k, k_out, stream)
+
+
+def hsa_rope_bwd(rope, pos, dq_out, dq, dk_out=None, dk=None, stream=None):
+    """Gradient of hsa_rope: dq, dk from the gradients dq_out, dk_out of its results."""
+    _rope_call("hsa_rope_bwd", rope, pos, dq_out, dq, dk_out, dk, stream)
+
+
+def make_quant(fmt=QUANT_E4M3, group=128) -> Quant:
+    return Quant(fmt, group)
+
+
+def hkv_quant_page_size(quant: Quant, P_tok: int, H: int, d: int):
+    """(bytes of a page of K or of V, byte offset of its scales)."""
+    n, off = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    _check(load_library().hkv_quant_page_size(ctypes.byref(quant), P_tok, H, d, ctypes.byref(n), ctypes.byref(off)),
+           "hkv_quant_page_size")
+    return n.value, off.value
+
+
+def _tables(where, device, page_k_ptrs, page_v_ptrs, ws):
+    NP = page_k_ptrs.numel()
+    return (_tensor(page_k_ptrs, "page_k_ptrs", where, device, torch.int64),
+            _tensor(page_v_ptrs, "page_v_ptrs", where, device, torch.int64, (NP,)), NP,
+            _tensor(ws, "ws", where, device, torch.uint8), ws.numel())
+
+
+def hkv_quant_rows(quant: Quant, K, V, page_k_ptrs, page_v_ptrs, P_tok, first_row, ws, first_row_dev=None, rope=None,
+                   pos=None, stream=None):
+    """Quantise rows K, V [T, H, d] (bfloat16, float16 or float32, strided as hsa_rope's) into history rows
+    first_row (+ first_row_dev, a device int64 scalar), ... of the pages; `rope` rotates the keys first."""
+    where, device, dtype = "hkv_quant_rows", K.device, K.dtype
+    if K.dim() != 3 or dtype not in _DTYPES:
+        _refuse(where, f"K is {list(K.shape)} {dtype}: [T, heads, d] bfloat16, float16 or float32 wanted")
+    T, _, d = K.shape
+    k, v = _rows(K, "K", where, device, dtype, T, d), _rows(V, "V", where, device, dtype, T, d)
+    pk, pv, NP, w, wn = _tables(where, device, page_k_ptrs, page_v_ptrs, ws)
+    r, at, step = _positions(rope, pos, where, device, T)
+    dev = None
+    if first_row_dev is not None:
+        dev = _tensor(first_row_dev.view(-1), "first_row_dev", where, device, torch.int64, (1,))
+    _on_device(device, lambda: _check(load_library().hkv_quant_rows(
+        ctypes.byref(quant), ctypes.byref(k), ctypes.byref(v), T, d, _DTYPES[dtype], r, at, step, pk, pv, NP, P_tok, first_row,
+        dev, w, wn, _stream(stream)), where))
+
+
+def hkv_gather_quant(quant: Quant, page_k_ptrs, page_v_ptrs, sel, Kp, P_tok, H, d, Kc, Vc, ws, kbar128=None, rope=None,
+                     pos=None, stream=None):
+    """hkv_gather from quantised pages; `rope` rotates active-cache row r by pos[:, r] (int32 [n_axes, Kp * P_tok])."""
+    where, device = "hkv_gather_quant", Kc.device
+    pk, pv, NP, w, wn = _tables(where, device, page_k_ptrs, page_v_ptrs, ws)
+    Lc = Kp * P_tok
+    s = _tensor(sel, "sel", where, device, torch.int32, (Kp,))
+    kc = _tensor(Kc, "Kc", where, device, torch.bfloat16, (Lc, H, d))
+    vc = _tensor(Vc, "Vc", where, device, torch.bfloat16, (Lc, H, d))
+    kb = None if kbar128 is None else _tensor(kbar128, "kbar128", where, device, torch.float32, (-(-Lc // 128), H, d))
+    r, at, step = _positions(rope, pos, where, device, Lc)
+    _on_device(device, lambda: _check(load_library().hkv_gather_quant(
+        ctypes.byref(quant), pk, pv, NP, s, Kp, P_tok, H, d, r, at, step, kc, vc, kb, w, wn, _stream(stream)), where))
+
+
+def hkv_attn_quant_workspace_size(T: int, Hq: int, H: int, d: int, Kp: int, P_tok: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().hkv_attn_quant_workspace_size(T, Hq, H, d, Kp, P_tok, ctypes.byref(n)),
+           "hkv_attn_quant_workspace_size")
+    return n.value
+
+
+def hkv_attn_quant(quant: Quant, Q, page_k_ptrs, page_v_ptrs, sel, Kp, P_tok, H, out, lse, ws, n_rows=None, scale=0.0,
+                   stream=None):
+    """Attention of a few queries Q [T, Hq, d] over the first n_rows (device int32 scalar; None: all) rows of the
+    selected pages of H heads.  out: [T, Hq, d] float32 or bfloat16; lse: [T, Hq] float32 or None."""
+    where, device = "hkv_attn_quant", Q.device
+    if Q.dim() != 3 or out.dtype not in (torch.float32, torch.bfloat16):
+        _refuse(where, f"Q is {list(Q.shape)}, out {out.dtype}: [T, heads, d], and float32 or bfloat16, wanted")
+    T, Hq, d = Q.shape
+    pk, pv, NP, w, wn = _tables(where, device, page_k_ptrs, page_v_ptrs, ws)
+    s = _tensor(sel, "sel", where, device, torch.int32, (Kp,))
+    q = _tensor(Q, "Q", where, device, torch.bfloat16)
+    o = _tensor(out, "out", where, device, out.dtype, Q.shape)
+    ls = None if lse is None else _tensor(lse, "lse", where, device, torch.float32, (T, Hq))
+    n = None if n_rows is None else _tensor(n_rows.view(-1), "n_rows", where, device, torch.int32, (1,))
+    _on_device(device, lambda: _check(load_library().hkv_attn_quant(
+        ctypes.byref(quant), q, T, Hq, pk, pv, NP, s, Kp, P_tok, H, d, n, scale, o, 1 if out.dtype == torch.bfloat16 else 0, ls,
+        w, wn, _stream(stream)), where))
 
 
 # ---------------------------------------------------------------- tracing

@@ -931,4 +931,282 @@ hsa_status_t hsa_forward_reuse(const hsa_config_t* cfg, const hsa_bf16* Q, const
                       out_is_bf16, sel_out, ws, ws_bytes, hsa::kProjChunk, false, stream);
 }
 
+// ------------------------------------------------------------------ rotary positions
+
+static int dtype_bytes(int dtype) {
+  return dtype == HSA_DTYPE_FP32 ? 4 : (dtype == HSA_DTYPE_BF16 || dtype == HSA_DTYPE_FP16) ? 2 : 0;
+}
+
+static hsa_status_t rope_args(const char* fn, const hsa_rope_t* rope, const int32_t* pos, long long pos_stride,
+                              long long tokens, int d, float sign, hsa::RopeArgs* out) {
+  memset(out, 0, sizeof(*out));
+  if (!rope) return HSA_OK;
+  if (rope->layout != HSA_ROPE_INTERLEAVED && rope->layout != HSA_ROPE_HALF)
+    return fail(HSA_ERR_INVALID_ARG, "%s: rope layout = %d", fn, rope->layout);
+  if (rope->rot_dim < 2 || rope->rot_dim > d)
+    return fail(HSA_ERR_INVALID_ARG, "%s: rot_dim = %d must be in [2, d = %d]", fn, rope->rot_dim, d);
+  if (rope->rot_dim % 16 != 0)
+    return fail(HSA_ERR_UNSUPPORTED, "%s: rot_dim = %d (supported: multiples of 16)", fn, rope->rot_dim);
+  if (rope->n_axes < 1 || rope->n_axes > 3) return fail(HSA_ERR_INVALID_ARG, "%s: n_axes = %d", fn, rope->n_axes);
+  const int pairs = rope->rot_dim / 2;
+  int end[3] = {pairs, pairs, pairs};
+  long long sum = 0;
+  for (int i = 0; i < rope->n_axes; ++i) {
+    if (rope->axis_pairs[i] < 0) return fail(HSA_ERR_INVALID_ARG, "%s: axis_pairs[%d] = %d", fn, i, rope->axis_pairs[i]);
+    sum += rope->axis_pairs[i];
+    if (sum > pairs) break;
+    if (i + 1 < rope->n_axes) end[i] = (int)sum;
+  }
+  if (sum != pairs) return fail(HSA_ERR_INVALID_ARG, "%s: the axes' pairs do not add up to rot_dim / 2 = %d", fn, pairs);
+  if (!isfinite(rope->mscale)) return fail(HSA_ERR_INVALID_ARG, "%s: mscale must be finite", fn);
+  REQUIRE_PTR(rope->inv_freq);
+  if (!pos && tokens > 0) return fail(HSA_ERR_INVALID_ARG, "%s: pos is NULL", fn);
+  if ((reinterpret_cast<uintptr_t>(pos) & 3u) != 0) return fail(HSA_ERR_INVALID_ARG, "%s: pos is not 4-byte aligned", fn);
+  if (rope->n_axes > 1 && pos_stride < tokens)
+    return fail(HSA_ERR_INVALID_ARG, "%s: pos_stride = %lld is below the tokens' %lld", fn, pos_stride, tokens);
+  out->on = true;
+  out->half_layout = rope->layout == HSA_ROPE_HALF;
+  out->pairs = pairs;
+  out->end0 = end[0];
+  out->end1 = end[1];
+  out->inv_freq = rope->inv_freq;
+  out->pos = pos;
+  out->pos_stride = pos_stride;
+  out->mscale = rope->mscale;
+  out->sign = sign;
+  return HSA_OK;
+}
+
+// Rows [T, H, d] of one tensor; `out` may not broadcast.
+static hsa_status_t rows_args(const char* fn, const char* what, const hsa_rows_t* x, int T, int d, int dtype, bool out,
+                              hsa::RowsArgs* r) {
+  if (!x || (!x->data && T > 0)) return fail(HSA_ERR_INVALID_ARG, "%s: %s is NULL", fn, what);
+  if (!aligned16(x->data)) return fail(HSA_ERR_INVALID_ARG, "%s: %s is not 16-byte aligned", fn, what);
+  TRY(check_heads(fn, x->H, d));
+  const long long unit = 16 / dtype_bytes(dtype);
+  if (x->token_stride % unit != 0 || x->head_stride % unit != 0)
+    return fail(HSA_ERR_INVALID_ARG, "%s: %s: strides %lld, %lld are not multiples of 16 bytes", fn, what, x->token_stride,
+                x->head_stride);
+  if (x->head_stride < d || x->token_stride < 0 || (out && T > 1 && x->token_stride < d))
+    return fail(HSA_ERR_INVALID_ARG, "%s: %s: strides %lld, %lld overlap (d = %d)", fn, what, x->token_stride,
+                x->head_stride, d);
+  r->data = x->data;
+  r->H = x->H;
+  r->token_stride = x->token_stride;
+  r->head_stride = x->head_stride;
+  return HSA_OK;
+}
+
+hsa_status_t hsa_rope_freqs(int dim, double base, int scaling, double factor, int orig_context, double* inv_freq,
+                            float* mscale) {
+  const char* fn = __func__;
+  if (dim < 2 || dim % 2 != 0) return fail(HSA_ERR_INVALID_ARG, "%s: dim = %d must be even and >= 2", fn, dim);
+  if (!(base > 1.0) || !isfinite(base)) return fail(HSA_ERR_INVALID_ARG, "%s: base must be finite and > 1", fn);
+  if (scaling < HSA_ROPE_SCALE_NONE || scaling > HSA_ROPE_SCALE_YARN)
+    return fail(HSA_ERR_INVALID_ARG, "%s: scaling = %d", fn, scaling);
+  if (scaling != HSA_ROPE_SCALE_NONE && (!(factor >= 1.0) || !isfinite(factor)))
+    return fail(HSA_ERR_INVALID_ARG, "%s: factor must be finite and >= 1", fn);
+  if (scaling == HSA_ROPE_SCALE_NTK && dim < 4) return fail(HSA_ERR_INVALID_ARG, "%s: NTK scaling needs dim >= 4", fn);
+  if (scaling == HSA_ROPE_SCALE_YARN && orig_context < 1)
+    return fail(HSA_ERR_INVALID_ARG, "%s: orig_context = %d must be >= 1", fn, orig_context);
+  if (!inv_freq) return fail(HSA_ERR_INVALID_ARG, "%s: inv_freq is NULL", fn);
+  if (scaling == HSA_ROPE_SCALE_NTK) base *= pow(factor, (double)dim / (dim - 2));
+  for (int i = 0; i < dim / 2; ++i) {
+    double f = pow(base, -2.0 * i / dim);
+    if (scaling == HSA_ROPE_SCALE_LINEAR) f /= factor;
+    if (scaling == HSA_ROPE_SCALE_YARN) {
+      const double turns = orig_context * f / 6.283185307179586477;
+      double keep = log(turns) / log(32.0);  // 0 at one turn, 1 at 32
+      keep = keep < 0.0 ? 0.0 : (keep > 1.0 ? 1.0 : keep);
+      f = f * keep + f / factor * (1.0 - keep);
+    }
+    inv_freq[i] = f;
+  }
+  if (mscale) *mscale = scaling == HSA_ROPE_SCALE_YARN ? (float)(0.1 * log(factor) + 1.0) : 1.0f;
+  return HSA_OK;
+}
+
+static hsa_status_t rope_impl(const char* fn, const hsa_rope_t* rope, const int32_t* pos, long long pos_stride, int T,
+                              int d, int dtype, const hsa_rows_t* q_in, const hsa_rows_t* q_out, const hsa_rows_t* k_in,
+                              const hsa_rows_t* k_out, float sign, hsa_stream_t stream) {
+  if (T < 0) return fail(HSA_ERR_INVALID_ARG, "%s: T = %d must be >= 0", fn, T);
+  if (!dtype_bytes(dtype)) return fail(HSA_ERR_INVALID_ARG, "%s: dtype = %d", fn, dtype);
+  if (!rope) return fail(HSA_ERR_INVALID_ARG, "%s: rope is NULL", fn);
+  if ((k_in == nullptr) != (k_out == nullptr)) return fail(HSA_ERR_INVALID_ARG, "%s: k_in and k_out go together", fn);
+  hsa::RowsArgs qi, qo, ki, ko;
+  memset(&ki, 0, sizeof(ki));
+  memset(&ko, 0, sizeof(ko));
+  TRY(rows_args(fn, "q_in", q_in, T, d, dtype, false, &qi));
+  TRY(rows_args(fn, "q_out", q_out, T, d, dtype, true, &qo));
+  if (qi.H != qo.H) return fail(HSA_ERR_INVALID_ARG, "%s: q_in has %d heads, q_out %d", fn, qi.H, qo.H);
+  if (k_in) {
+    TRY(rows_args(fn, "k_in", k_in, T, d, dtype, false, &ki));
+    TRY(rows_args(fn, "k_out", k_out, T, d, dtype, true, &ko));
+    if (ki.H != ko.H) return fail(HSA_ERR_INVALID_ARG, "%s: k_in has %d heads, k_out %d", fn, ki.H, ko.H);
+  }
+  hsa::RopeArgs r;
+  TRY(rope_args(fn, rope, pos, pos_stride, T, d, sign, &r));
+  if (T == 0) return HSA_OK;
+  HSA_LAUNCH("rope", hsa::launch_rope(r, T, d, dtype, qi, qo, ki, ko, stream));
+  return HSA_OK;
+}
+
+hsa_status_t hsa_rope(const hsa_rope_t* rope, const int32_t* pos, long long pos_stride, int T, int d, int dtype,
+                      const hsa_rows_t* q_in, const hsa_rows_t* q_out, const hsa_rows_t* k_in, const hsa_rows_t* k_out,
+                      hsa_stream_t stream) {
+  return rope_impl(__func__, rope, pos, pos_stride, T, d, dtype, q_in, q_out, k_in, k_out, 1.f, stream);
+}
+
+hsa_status_t hsa_rope_bwd(const hsa_rope_t* rope, const int32_t* pos, long long pos_stride, int T, int d, int dtype,
+                          const hsa_rows_t* q_in, const hsa_rows_t* q_out, const hsa_rows_t* k_in,
+                          const hsa_rows_t* k_out, hsa_stream_t stream) {
+  return rope_impl(__func__, rope, pos, pos_stride, T, d, dtype, q_in, q_out, k_in, k_out, -1.f, stream);
+}
+
+// ------------------------------------------------------------------ quantised pages
+
+static hsa_status_t quant_args(const char* fn, const hkv_quant_t* q, int P_tok, int H, int d, hsa::QuantArgs* out) {
+  if (t_fault == HSA_FAULT_ARG) return fail(HSA_ERR_INVALID_ARG, "%s: injected argument failure", fn);
+  if (!q) return fail(HSA_ERR_INVALID_ARG, "%s: quant is NULL", fn);
+  TRY(check_heads(fn, H, d));
+  if (P_tok < 1) return fail(HSA_ERR_INVALID_ARG, "%s: P_tok = %d must be >= 1", fn, P_tok);
+  if (q->format < HKV_QUANT_E4M3 || q->format > HKV_QUANT_INT4)
+    return fail(HSA_ERR_INVALID_ARG, "%s: quant format = %d", fn, q->format);
+  if (q->group != 32 && q->group != 64 && q->group != 128)
+    return fail(HSA_ERR_UNSUPPORTED, "%s: quant group = %d (supported: 32, 64, 128)", fn, q->group);
+  if (q->group > d) return fail(HSA_ERR_INVALID_ARG, "%s: quant group = %d is above d = %d", fn, q->group, d);
+  out->format = q->format;
+  out->group = q->group;
+  out->P_tok = P_tok;
+  out->H = H;
+  out->d = d;
+  const long long codes = (long long)P_tok * H * d / (q->format == HKV_QUANT_INT4 ? 2 : 1);
+  out->scale_offset = (codes + 255) / 256 * 256;
+  return HSA_OK;
+}
+
+hsa_status_t hkv_quant_page_size(const hkv_quant_t* q, int P_tok, int H, int d, size_t* page_bytes,
+                                 size_t* scale_offset) {
+  const char* fn = __func__;
+  hsa::QuantArgs a;
+  TRY(quant_args(fn, q, P_tok, H, d, &a));
+  if (!page_bytes) return fail(HSA_ERR_INVALID_ARG, "%s: page_bytes is NULL", fn);
+  const size_t bytes = (size_t)a.scale_offset + (size_t)P_tok * H * (d / a.group) * sizeof(float);
+  *page_bytes = (bytes + 1023) / 1024 * 1024;
+  if (scale_offset) *scale_offset = (size_t)a.scale_offset;
+  return HSA_OK;
+}
+
+hsa_status_t hkv_quant_rows(const hkv_quant_t* q, const hsa_rows_t* K, const hsa_rows_t* V, int T, int d, int dtype,
+                            const hsa_rope_t* rope, const int32_t* pos, long long pos_stride, void* const* page_k,
+                            void* const* page_v, int NP, int P_tok, long long first_row, const long long* first_row_dev,
+                            void* ws, size_t ws_bytes, hsa_stream_t stream) {
+  const char* fn = __func__;
+  if (T < 0) return fail(HSA_ERR_INVALID_ARG, "%s: T = %d must be >= 0", fn, T);
+  if (!dtype_bytes(dtype)) return fail(HSA_ERR_INVALID_ARG, "%s: dtype = %d", fn, dtype);
+  hsa::RowsArgs k, v;
+  TRY(rows_args(fn, "K", K, T, d, dtype, false, &k));
+  TRY(rows_args(fn, "V", V, T, d, dtype, false, &v));
+  if (k.H != v.H) return fail(HSA_ERR_INVALID_ARG, "%s: K has %d heads, V %d", fn, k.H, v.H);
+  hsa::QuantArgs a;
+  TRY(quant_args(fn, q, P_tok, k.H, d, &a));
+  hsa::RopeArgs r;
+  TRY(rope_args(fn, rope, pos, pos_stride, T, d, 1.f, &r));
+  if (NP < 1) return fail(HSA_ERR_INVALID_ARG, "%s: NP = %d must be >= 1", fn, NP);
+  if (!page_k || !page_v) return fail(HSA_ERR_INVALID_ARG, "%s: NULL page table", fn);
+  if (!first_row_dev && (first_row < 0 || first_row > (long long)NP * P_tok - T))
+    return fail(HSA_ERR_INVALID_ARG, "%s: rows [%lld, %lld) outside the %d pages of %d", fn, first_row, first_row + T, NP,
+                P_tok);
+  if (first_row < -hsa::kQuantMaxRow || first_row > hsa::kQuantMaxRow)
+    return fail(HSA_ERR_INVALID_ARG, "%s: first_row = %lld", fn, first_row);
+  OPTIONAL_PTR8(first_row_dev);
+  TRY(check_ws(fn, ws, ws_bytes, 256));
+  if (T == 0) return HSA_OK;
+  HSA_LAUNCH("quant_rows", hsa::launch_quant_rows(a, r, k, v, T, dtype, page_k, page_v, NP, first_row, first_row_dev,
+                                                  status_of(ws), stream));
+  return HSA_OK;
+}
+
+hsa_status_t hkv_gather_quant(const hkv_quant_t* q, const void* const* page_k, const void* const* page_v, int NP,
+                              const int32_t* sel, int Kp, int P_tok, int H, int d, const hsa_rope_t* rope,
+                              const int32_t* pos, long long pos_stride, hsa_bf16* Kc, hsa_bf16* Vc, float* kbar128,
+                              void* ws, size_t ws_bytes, hsa_stream_t stream) {
+  const char* fn = __func__;
+  hsa::QuantArgs a;
+  TRY(quant_args(fn, q, P_tok, H, d, &a));
+  if (NP < 1) return fail(HSA_ERR_INVALID_ARG, "%s: NP = %d must be >= 1", fn, NP);
+  if (Kp < 1 || Kp > NP) return fail(HSA_ERR_INVALID_ARG, "%s: Kp = %d must be in [1, NP]", fn, Kp);
+  if (!page_k || !page_v || !sel) return fail(HSA_ERR_INVALID_ARG, "%s: NULL page table or selection", fn);
+  REQUIRE_PTR(Kc);
+  REQUIRE_PTR(Vc);
+  OPTIONAL_PTR(kbar128);
+  hsa::RopeArgs r;
+  TRY(rope_args(fn, rope, pos, pos_stride, (long long)Kp * P_tok, d, 1.f, &r));
+  TRY(check_ws(fn, ws, ws_bytes, 256));
+  HSA_LAUNCH("gather_quant", hsa::launch_gather_quant(a, r, page_k, page_v, NP, sel, Kp, Kc, Vc, kbar128, status_of(ws),
+                                                      stream));
+  return HSA_OK;
+}
+
+static hsa_status_t attn_quant_layout(const char* fn, int T, int Hq, int H, int d, int Kp, int P_tok, int* splits,
+                                      size_t* part_ml, size_t* total) {
+  TRY(check_heads(fn, H, d));
+  if (T < 0) return fail(HSA_ERR_INVALID_ARG, "%s: T = %d must be >= 0", fn, T);
+  if (T > 64) return fail(HSA_ERR_UNSUPPORTED, "%s: T = %d queries (supported: up to 64; assemble the cache for more)", fn, T);
+  if (Hq < 1 || Hq % H != 0) return fail(HSA_ERR_INVALID_ARG, "%s: Hq = %d is not a multiple of H = %d", fn, Hq, H);
+  if (Kp < 1 || P_tok < 1) return fail(HSA_ERR_INVALID_ARG, "%s: Kp = %d, P_tok = %d must be >= 1", fn, Kp, P_tok);
+  if ((long long)Kp * P_tok > 0x7fffffffLL)
+    return fail(HSA_ERR_UNSUPPORTED, "%s: Kp * P_tok = %lld rows exceed 2^31 - 1", fn, (long long)Kp * P_tok);
+  *splits = T > 0 ? hsa::attn_quant_splits(T, Hq, H, d, Kp, P_tok) : 1;
+  const size_t rows = *splits > 1 ? (size_t)*splits * T * Hq : 0;
+  *part_ml = 256 + align256(rows * d * sizeof(float));
+  *total = *part_ml + align256(rows * sizeof(float2));
+  return HSA_OK;
+}
+
+hsa_status_t hkv_attn_quant_workspace_size(int T, int Hq, int H, int d, int Kp, int P_tok, size_t* bytes) {
+  const char* fn = __func__;
+  if (!bytes) return fail(HSA_ERR_INVALID_ARG, "%s: bytes is NULL", fn);
+  int splits;
+  size_t part_ml;
+  return attn_quant_layout(fn, T, Hq, H, d, Kp, P_tok, &splits, &part_ml, bytes);
+}
+
+hsa_status_t hkv_attn_quant(const hkv_quant_t* q, const hsa_bf16* Q, int T, int Hq, const void* const* page_k,
+                            const void* const* page_v, int NP, const int32_t* sel, int Kp, int P_tok, int H, int d,
+                            const int32_t* n_rows, float scale, void* out, int out_is_bf16, float* lse, void* ws,
+                            size_t ws_bytes, hsa_stream_t stream) {
+  const char* fn = __func__;
+  hsa::AttnQuantArgs a;
+  memset(&a, 0, sizeof(a));
+  TRY(quant_args(fn, q, P_tok, H, d, &a.q));
+  size_t part_ml, total;
+  TRY(attn_quant_layout(fn, T, Hq, H, d, Kp, P_tok, &a.splits, &part_ml, &total));
+  if (NP < 1 || Kp > NP) return fail(HSA_ERR_INVALID_ARG, "%s: Kp = %d must be in [1, NP = %d]", fn, Kp, NP);
+  if (!page_k || !page_v || !sel) return fail(HSA_ERR_INVALID_ARG, "%s: NULL page table or selection", fn);
+  if (!(scale >= 0.f) || isinf(scale)) return fail(HSA_ERR_INVALID_ARG, "%s: scale must be finite and >= 0", fn);
+  TRY(check_ws(fn, ws, ws_bytes, total));
+  if (T == 0) return HSA_OK;
+  REQUIRE_PTR(Q);
+  REQUIRE_PTR(out);
+  a.Q = Q;
+  a.T = T;
+  a.Hq = Hq;
+  a.page_k = page_k;
+  a.page_v = page_v;
+  a.NP = NP;
+  a.sel = sel;
+  a.Kp = Kp;
+  a.n_rows = n_rows;
+  a.scale_log2e = (scale > 0.f ? scale : 1.0f / sqrtf((float)d)) * 1.44269504088896340736f;
+  if (out_is_bf16) a.out_bf16 = static_cast<uint16_t*>(out);
+  else a.out_f32 = static_cast<float*>(out);
+  a.lse = lse;
+  a.part_o = at<float>(ws, 256);
+  a.part_ml = at<float2>(ws, part_ml);
+  a.status = status_of(ws);
+  HSA_LAUNCH("attn_quant", hsa::launch_attn_quant(a, stream));
+  return HSA_OK;
+}
+
 }  // extern "C"

@@ -170,6 +170,66 @@ constexpr int kFidelitySplits = 64;
 cudaError_t launch_fidelity(const float* o_ref, const float* lse_ref, const float* o_sp, const float* lse_sp,
                             const float* o_lin, int Lq, int H, int d, double* part, double* report, cudaStream_t s);
 
+// ---------------------------------------------------------------- rope.cu
+// Rotary positions as the kernels take them (hsa_rope_t, checked by the entry points).
+struct RopeArgs {
+  bool on;           // false: nothing is rotated, the rest is not read
+  bool half_layout;
+  int pairs;         // rot_dim / 2
+  int end0, end1;    // first pair of the second and of the third axis
+  const double* inv_freq;
+  const int32_t* pos;  // [axis][token], rows pos_stride apart
+  long long pos_stride;
+  float mscale;
+  float sign;        // -1: backward
+};
+struct RowsArgs {
+  void* data;
+  int H;
+  long long token_stride, head_stride;
+};
+int rope_head_groups(long long tokens, int J, int heads);
+cudaError_t launch_rope(const RopeArgs& r, int tokens, int d, int dtype, const RowsArgs& q_in, const RowsArgs& q_out,
+                        const RowsArgs& k_in, const RowsArgs& k_out, cudaStream_t s);
+
+// ---------------------------------------------------------------- quant.cu
+// Quantised pages (layout in include/hsa.h).
+struct QuantArgs {
+  int format, group;
+  int P_tok, H, d;
+  long long scale_offset;  // bytes
+};
+constexpr long long kQuantMaxRow = 1LL << 61;  // magnitudes of a first row that can be added up in 64 bits
+cudaError_t launch_quant_rows(const QuantArgs& q, const RopeArgs& r, const RowsArgs& K, const RowsArgs& V, int tokens,
+                              int dtype, void* const* page_k, void* const* page_v, int NP, long long first_row,
+                              const long long* first_row_dev, int* status, cudaStream_t s);
+cudaError_t launch_gather_quant(const QuantArgs& q, const RopeArgs& r, const void* const* page_k,
+                                const void* const* page_v, int NP, const int32_t* sel, int Kp, uint16_t* Kc,
+                                uint16_t* Vc, float* kbar128, int* status, cudaStream_t s);
+
+// ---------------------------------------------------------------- attn_quant.cu
+struct AttnQuantArgs {
+  QuantArgs q;
+  const uint16_t* Q;  // [T][Hq][d]
+  int T, Hq;
+  const void* const* page_k;
+  const void* const* page_v;
+  int NP;
+  const int32_t* sel;
+  int Kp;
+  const int32_t* n_rows;  // device, may be NULL
+  float scale_log2e;      // softmax scale x log2(e)
+  float* out_f32;         // one of the two
+  uint16_t* out_bf16;
+  float* lse;             // may be NULL
+  int splits;
+  float* part_o;          // [splits][T * Hq][d], unused when splits == 1
+  float2* part_ml;        // [splits][T * Hq] (max in log2 units, sum)
+  int* status;
+};
+int attn_quant_splits(int T, int Hq, int H, int d, int Kp, int P_tok);
+cudaError_t launch_attn_quant(const AttnQuantArgs& a, cudaStream_t s);
+
 // ---------------------------------------------------------------- waits.cu
 // Write the wait limit (microseconds; 0 = the 2 s default) into a workspace header.
 cudaError_t launch_set_wait_limit(int* header, uint32_t limit_us, cudaStream_t s);

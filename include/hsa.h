@@ -367,6 +367,151 @@ hsa_status_t hkv_store_prefetch(const hkv_store_t* st, const float* scores, cons
 hsa_status_t hkv_store_residency(const hkv_store_t* st, int32_t* slot_of_page, int32_t* page_of_slot,
                                  hsa_stream_t stream);
 
+/* ------------------------------------------------- rotary positions ---- */
+
+/* Element types of the calls that take more than bf16. */
+#define HSA_DTYPE_BF16 0
+#define HSA_DTYPE_FP16 1
+#define HSA_DTYPE_FP32 2
+
+/* Rotary positions of queries and keys (the video backbone rotates both by their
+ * frame, row and column before the attention; the attention entry points take
+ * tensors that are already rotated).  Pair p of a token's head turns by the angle
+ *   theta_p = pos[axis(p)][token] * inv_freq[p]
+ * and is multiplied by mscale:
+ *   y_a = mscale (x_a cos theta - x_b sin theta),  y_b = mscale (x_b cos theta + x_a sin theta)
+ * where (a, b) = (2p, 2p + 1) in HSA_ROPE_INTERLEAVED and (p, p + rot_dim / 2) in
+ * HSA_ROPE_HALF.  Columns from rot_dim on are copied as they are.  Angles are formed
+ * and reduced in fp64 (positions may be far: the whole int32 range), the rotation is
+ * done in fp32 and rounded once to the output type. */
+#define HSA_ROPE_INTERLEAVED 0
+#define HSA_ROPE_HALF 1
+typedef struct {
+  int layout;              /* HSA_ROPE_INTERLEAVED or HSA_ROPE_HALF */
+  int rot_dim;             /* rotated columns of a head: a multiple of 16 in [16, d] */
+  int n_axes;              /* position axes, 1 to 3 */
+  int axis_pairs[3];       /* pairs of each axis, in order; they add up to rot_dim / 2 */
+  float mscale;            /* factor on cos and sin (1 unless the scaling asks for one); finite */
+  const double* inv_freq;  /* device fp64 [rot_dim / 2]: radians a position */
+} hsa_rope_t;
+
+/* One tensor of token rows [T, H, d] inside a larger one: element (t, h, c) is at
+ * data[t * token_stride + h * head_stride + c].  data is 16-byte aligned and the
+ * strides (in elements) are multiples of 16 bytes, head_stride >= d and
+ * token_stride >= 0 (0 broadcasts one row; not for outputs). */
+typedef struct {
+  void* data;
+  int H;
+  long long token_stride;
+  long long head_stride;
+} hsa_rows_t;
+
+/* inv_freq of one axis of `dim` rotated columns (dim / 2 values into HOST memory):
+ * base^(-2i / dim), and for contexts longer than the trained one:
+ *   HSA_ROPE_SCALE_LINEAR  divided by factor (position interpolation)
+ *   HSA_ROPE_SCALE_NTK     base raised to base * factor^(dim / (dim - 2)); dim >= 4
+ *   HSA_ROPE_SCALE_YARN    by wavelength: pairs that turn more than 32 times in
+ *                          orig_context positions are kept, pairs that turn less than
+ *                          once are divided by factor, those between are blended
+ *                          linearly in the logarithm of their turns
+ * mscale (optional, host) receives the factor for hsa_rope_t.mscale: 0.1 ln(factor) + 1
+ * for YARN, else 1.  factor >= 1.  Host-only, launches nothing. */
+#define HSA_ROPE_SCALE_NONE 0
+#define HSA_ROPE_SCALE_LINEAR 1
+#define HSA_ROPE_SCALE_NTK 2
+#define HSA_ROPE_SCALE_YARN 3
+hsa_status_t hsa_rope_freqs(int dim, double base, int scaling, double factor, int orig_context, double* inv_freq,
+                            float* mscale);
+
+/* y = rotated x for the tokens' queries and, in the same pass, their keys (k_in and
+ * k_out NULL: queries only).  pos: device int32 [n_axes][T] (rows pos_stride elements
+ * apart, pos_stride >= T).  q_out / k_out may be q_in / k_in (in place, same strides);
+ * other overlaps are not allowed.  T may be 0 (nothing is launched).  d in {64, 128}. */
+hsa_status_t hsa_rope(const hsa_rope_t* rope, const int32_t* pos, long long pos_stride, int T, int d, int dtype,
+                      const hsa_rows_t* q_in, const hsa_rows_t* q_out, const hsa_rows_t* k_in,
+                      const hsa_rows_t* k_out, hsa_stream_t stream);
+
+/* The gradient of hsa_rope: given dL/dy in q_in / k_in, writes dL/dx = mscale R(-theta)
+ * dL/dy to q_out / k_out (the columns from rot_dim on are copied). */
+hsa_status_t hsa_rope_bwd(const hsa_rope_t* rope, const int32_t* pos, long long pos_stride, int T, int d, int dtype,
+                          const hsa_rows_t* q_in, const hsa_rows_t* q_out, const hsa_rows_t* k_in,
+                          const hsa_rows_t* k_out, hsa_stream_t stream);
+
+/* ------------------------------------------------- quantised history pages ---- */
+
+/* History pages in 8 or 4 bits: half or a quarter of the HBM slots, the host tier and
+ * the host link's traffic of bf16 pages.  Each group of `group` consecutive columns of
+ * one row and head has one fp32 scale:
+ *   a = max |x| over the group;  scale = a / qmax;  code = round(x * (qmax / a))
+ * (the quotients and the product in fp32, rounding to nearest even) with qmax = 448
+ * (HKV_QUANT_E4M3), 127 (HKV_QUANT_INT8) or 7 (HKV_QUANT_INT4), and is read back as
+ * code * scale.  A group with a < 2^-100 is stored as zeros (scale 0).  A group with an
+ * infinity or a NaN is stored with a NaN scale: it reads back as NaN throughout.
+ *
+ * A page of P_tok rows is one block of hkv_quant_page_size() bytes (16-byte aligned):
+ *   [0, ...)             codes [P_tok][H][d], 1 byte each, or two to a byte in 4 bits
+ *                        (column 2i in the low half of byte i, two's complement)
+ *   [scale_offset, ...)  fp32 scales [P_tok][H][d / group]; scale_offset is the end of
+ *                        the codes rounded up to 256 bytes
+ * The size is a multiple of 1024, so an hkv_store_t of P_tok = page_bytes / 1024, H = 4,
+ * d = 128 keeps such pages in its two tiers: every hkv_store_* call but
+ * hkv_store_seal works on it as on bf16 pages (hkv_quant_rows writes the host tier). */
+#define HKV_QUANT_E4M3 0
+#define HKV_QUANT_INT8 1
+#define HKV_QUANT_INT4 2
+typedef struct {
+  int format;  /* HKV_QUANT_* */
+  int group;   /* columns a scale covers: 32, 64 or 128, at most d */
+} hkv_quant_t;
+
+/* Bytes of one page of K (or of V) and the offset of its scales.  Host-only. */
+hsa_status_t hkv_quant_page_size(const hkv_quant_t* q, int P_tok, int H, int d, size_t* page_bytes,
+                                 size_t* scale_offset);
+
+/* Append T rows to the paged history: row t becomes history row g = first_row + t
+ * (+ *first_row_dev, an optional device int64, e.g. a captured decode step's position),
+ * that is row g % P_tok of page g / P_tok.  K, V: [T, H, d] of `dtype` (strides as in
+ * hsa_rows_t).  rope (optional): the keys are rotated first, at pos [n_axes][T]
+ * (absolute positions; leave it NULL for pages whose keys are rotated when they are
+ * read).  page_k / page_v: device arrays of NP page addresses (device memory or mapped
+ * page-locked host memory).  Rows of other tokens are left as they are.  A row outside
+ * [0, NP * P_tok) or a NULL or misaligned page sets HSA_ERR_DEVICE and is skipped.
+ * T may be 0.  Uses the workspace (status). */
+hsa_status_t hkv_quant_rows(const hkv_quant_t* q, const hsa_rows_t* K, const hsa_rows_t* V, int T, int d, int dtype,
+                            const hsa_rope_t* rope, const int32_t* pos, long long pos_stride, void* const* page_k,
+                            void* const* page_v, int NP, int P_tok, long long first_row, const long long* first_row_dev,
+                            void* ws, size_t ws_bytes, hsa_stream_t stream);
+
+/* Active-cache assembly from quantised pages, as hkv_gather: for i < Kp,
+ *   Vc[i*P_tok + t] = bf16(page_v[sel[i]][t]),  Kc[i*P_tok + t] = bf16(rotated page_k[sel[i]][t])
+ * rope (optional): active-cache row r is rotated at pos[..][r], pos [n_axes][Kp*P_tok]
+ * (a retrieved page moves to another place in the active cache).  One rounding, from
+ * fp32.  kbar128 (optional): [ceil(Lc/128), H, d] fp32 block means of the keys, taken
+ * before that rounding.  A bad page id or page address sets HSA_ERR_DEVICE; its rows are
+ * left as they were and count as zeros in kbar128.  Uses the workspace (status). */
+hsa_status_t hkv_gather_quant(const hkv_quant_t* q, const void* const* page_k, const void* const* page_v, int NP,
+                              const int32_t* sel, int Kp, int P_tok, int H, int d, const hsa_rope_t* rope,
+                              const int32_t* pos, long long pos_stride, hsa_bf16* Kc, hsa_bf16* Vc, float* kbar128,
+                              void* ws, size_t ws_bytes, hsa_stream_t stream);
+
+/* Attention of a few query tokens straight over the selected quantised pages (single
+ * tokens, prompt or action tokens: the bf16 active cache is not assembled):
+ *   o[t, h] = sum_r softmax_r(scale q[t, h] . k_r) v_r,  lse[t, h] = ln sum_r exp(scale q . k_r)
+ * over the first n rows of pages sel[0..Kp) in order, n = min(*n_rows, Kp * P_tok)
+ * (n_rows: optional device int32; NULL: all rows), with k_r, v_r of key head
+ * h / (Hq / H).  Keys are used as stored (rotate them as they are written).  Q:
+ * [T, Hq, d] bf16, Hq a multiple of H; out: [T, Hq, d] fp32, or bf16 when out_is_bf16;
+ * lse (optional): [T, Hq] fp32.  scale: 0 means 1/sqrt(d).  n = 0 gives o = 0 and lse =
+ * -inf; a bad page sets HSA_ERR_DEVICE and its rows are not attended to.  Two results
+ * over disjoint rows merge by their lse.  T <= 64; for a whole chunk assemble the cache
+ * and use hsa_forward.  T may be 0.  Deterministic.  Workspace:
+ * hkv_attn_quant_workspace_size() bytes, its 256-byte header as every workspace's. */
+hsa_status_t hkv_attn_quant_workspace_size(int T, int Hq, int H, int d, int Kp, int P_tok, size_t* bytes);
+hsa_status_t hkv_attn_quant(const hkv_quant_t* q, const hsa_bf16* Q, int T, int Hq, const void* const* page_k,
+                            const void* const* page_v, int NP, const int32_t* sel, int Kp, int P_tok, int H, int d,
+                            const int32_t* n_rows, float scale, void* out, int out_is_bf16, float* lse,
+                            void* ws, size_t ws_bytes, hsa_stream_t stream);
+
 /* ---------------------------------------------------------------- HSA ---- */
 
 /* Head-adaptive block selection ([NEWS] HSA paragraph).  Pools Q and Kc into
