@@ -57,10 +57,10 @@ __device__ __forceinline__ void write_chunk(const QuantArgs& q, char* page, long
   const bool finite = amax < 0x7f800000u;
   const float a = __uint_as_float(amax);
   const bool kept = finite && a >= kQuantTiny;
-  const float inv = kept ? __fdiv_rn(qmax_of<FMT>(), a) : 0.f;
+  const float inv = kept ? __fmul_rn(__frcp_rn(a), qmax_of<FMT>()) : 0.f;
   store_codes<FMT>(page + (head_row * q.d + chunk * 8) * code_bits<FMT>() / 8, encode8<FMT>(f, inv, finite));
   if (chunk * 8 % q.group == 0) {
-    const float scale = kept ? __fdiv_rn(a, qmax_of<FMT>()) : (finite ? 0.f : __uint_as_float(0x7fc00000u));
+    const float scale = kept ? __fmul_rn(a, 1.f / qmax_of<FMT>()) : (finite ? 0.f : __uint_as_float(0x7fc00000u));
     reinterpret_cast<float*>(page + q.scale_offset)[head_row * (q.d / q.group) + chunk * 8 / q.group] = scale;
   }
 }

@@ -92,7 +92,7 @@ __device__ __forceinline__ Codes8<FMT> encode8(const float* f, float inv, bool f
       c.w[k] = finite ? w : 0u;
     }
   } else {
-    // x * inv is at most qmax (1 + 2^-23) in magnitude, so the rounded integer is at most
+    // x * inv is at most qmax (1 + 2^-20) in magnitude, so the rounded integer is at most
     // qmax.  It is read from the mantissa of 1.5 * 2^23 + x, whose addition rounds to the
     // nearest integer, ties to even.
     uint32_t u[8];

@@ -442,8 +442,8 @@ hsa_status_t hsa_rope_bwd(const hsa_rope_t* rope, const int32_t* pos, long long 
 /* History pages in 8 or 4 bits: half or a quarter of the HBM slots, the host tier and
  * the host link's traffic of bf16 pages.  Each group of `group` consecutive columns of
  * one row and head has one fp32 scale:
- *   a = max |x| over the group;  scale = a / qmax;  code = round(x * (qmax / a))
- * (the quotients and the product in fp32, rounding to nearest even) with qmax = 448
+ *   a = max |x| over the group;  scale = a * (1 / qmax);  code = round(x * (qmax * (1 / a)))
+ * (reciprocals and products each rounded to fp32, rounding to nearest even) with qmax = 448
  * (HKV_QUANT_E4M3), 127 (HKV_QUANT_INT8) or 7 (HKV_QUANT_INT4), and is read back as
  * code * scale.  A group with a < 2^-100 is stored as zeros (scale 0).  A group with an
  * infinity or a NaN is stored with a NaN scale: it reads back as NaN throughout.

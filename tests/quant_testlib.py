@@ -36,8 +36,8 @@ def encode(x, fmt, group):
     a = q.abs().amax(-1)
     kept = torch.isfinite(a) & (a >= 2.0 ** -100)
     qmax = torch.tensor(QMAX[fmt])
-    scale = torch.where(kept, a / qmax, torch.zeros(()))
-    inv = torch.where(kept, qmax / a, torch.zeros(()))
+    scale = torch.where(kept, a * torch.reciprocal(qmax), torch.zeros(()))
+    inv = torch.where(kept, torch.reciprocal(a) * qmax, torch.zeros(()))
     finite = torch.isfinite(q).all(-1)
     scale = torch.where(finite, scale, torch.full((), float("nan")))
     v = q * inv[..., None]
