@@ -35,6 +35,13 @@ namespace {
 
 constexpr int kAqWarps = 4;
 constexpr int kAqThreads = kAqWarps * 32;
+#ifndef AQ_S
+#define AQ_S 3
+#define AQ_C 3
+#endif
+constexpr int kAqStages = AQ_S;  // tiles of a warp's ring
+constexpr int kAqCtas = AQ_C;    // on an SM
+constexpr int kAqCtasWide = 2;   // ... with 16 queries to a tile
 
 __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -59,29 +66,28 @@ __device__ __forceinline__ uint32_t hsub2_u(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&d);
 }
 
-// N bytes of codes a thread loads at once, as words (N = 2: the low half of one).
+// N bytes of codes a thread reads at once, as words (N = 2: the low half of one).
 template <int N>
 struct Raw {
   uint32_t w[(N + 3) / 4];
 };
 template <int N>
-__device__ __forceinline__ Raw<N> load_raw(const void* p) {
+__device__ __forceinline__ Raw<N> read_raw(const char* p) {
   Raw<N> r;
   if constexpr (N >= 16) {
 #pragma unroll
     for (int i = 0; i < N / 16; ++i) {
-      const uint4 v = ld_nc_v4(static_cast<const char*>(p) + 16 * i);
+      const uint4 v = *reinterpret_cast<const uint4*>(p + 16 * i);
       r.w[4 * i] = v.x; r.w[4 * i + 1] = v.y; r.w[4 * i + 2] = v.z; r.w[4 * i + 3] = v.w;
     }
   } else if constexpr (N == 8) {
-    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(r.w[0]), "=r"(r.w[1]) : "l"(p));
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    r.w[0] = v.x; r.w[1] = v.y;
   } else if constexpr (N == 4) {
-    asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(r.w[0]) : "l"(p));
+    r.w[0] = *reinterpret_cast<const uint32_t*>(p);
   } else {
     static_assert(N == 2, "2, 4, 8 or a multiple of 16 bytes");
-    uint16_t h;
-    asm volatile("ld.global.nc.L1::no_allocate.u16 %0, [%1];" : "=h"(h) : "l"(p));
-    r.w[0] = h;
+    r.w[0] = *reinterpret_cast<const uint16_t*>(p);
   }
   return r;
 }
@@ -137,15 +143,25 @@ __device__ __forceinline__ float pow2_below(float x) {  // the power of two at o
 }
 __device__ __forceinline__ float pow2_inverse(float p) { return __uint_as_float((254u << 23) - __float_as_uint(p)); }
 
+// A warp's ring of 16-key tiles in shared memory: codes of K and of V, rows padded by 16 bytes
+// (the operand reads below are then free of bank conflicts at 128-byte rows), and scales.
+template <int FMT, int D, int GROUP>
+struct Stage {
+  static constexpr int kRow = D * code_bits<FMT>() / 8, kPitch = kRow + 16;
+  static constexpr int kScales = 16 * (D / GROUP) * 4;  // bytes of a tile's
+  static constexpr int kV = 16 * kPitch, kKs = 2 * kV, kVs = kKs + kScales, kBytes = kVs + kScales;
+};
+
 template <int FMT, int D, int GROUP, int NT>
-__global__ void __launch_bounds__(kAqThreads) attn_quant_kernel(const AttnQuantArgs a) {
+__global__ void __launch_bounds__(kAqThreads, NT == 1 ? kAqCtas : kAqCtasWide) attn_quant_kernel(const AttnQuantArgs a) {
   constexpr int G = D / GROUP;               // groups of a head
   constexpr int KS = GROUP / 16;             // product steps of a group (S), and 16-column tiles of a group (O)
   constexpr int BITS = code_bits<FMT>();
-  constexpr int KB = GROUP / 4 * BITS / 8;   // bytes of a group a thread loads of a key row
+  constexpr int KB = GROUP / 4 * BITS / 8;   // bytes of a group a thread reads of a key row
   constexpr int VB = GROUP / 8 * BITS / 8;   // ... of a value row
   constexpr int COLS = 8 * NT;               // queries of a tile
-  __shared__ float s_o[COLS][D];
+  using St = Stage<FMT, D, GROUP>;
+  extern __shared__ __align__(16) char ring_all[];
   __shared__ float s_m[kAqWarps][COLS], s_l[kAqWarps][COLS];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int g = lane / 4, t = lane % 4;
@@ -153,6 +169,71 @@ __global__ void __launch_bounds__(kAqThreads) attn_quant_kernel(const AttnQuantA
   const int share = a.Hq / a.q.H;            // query heads of this key head
   const int cols = a.T * share, col0 = blockIdx.y * COLS;
   const int P = a.q.P_tok;
+
+  // Tiles of the first n rows: tiles_page of each whole page, then those of the last one.
+  const long long all = (long long)a.Kp * P;
+  long long n_rows = a.n_rows ? (long long)*a.n_rows : all;
+  n_rows = n_rows < 0 ? 0 : (n_rows > all ? all : n_rows);
+  const int tiles_page = (P + 15) / 16;
+  const int whole = (int)(n_rows / P), rest = (int)(n_rows - (long long)whole * P);
+  const int tiles = whole * tiles_page + (rest + 15) / 16;
+  const int per = (tiles + a.splits - 1) / a.splits;
+  const int tile_end = (int)min((long long)tiles, (long long)(split + 1) * per);
+
+  // asking for tiles: this warp's are warp, warp + kAqWarps, ... of the split's
+  char* ring = ring_all + warp * kAqStages * St::kBytes;
+  const uint32_t ring_s = smem_u32(ring);
+  constexpr int CH = St::kRow / 16;          // 16-byte vectors of a row
+  constexpr int PER = 16 * CH / 32;          // ... of a tile that a lane copies
+  const int my_row = lane / CH, my_vec = lane % CH;
+  const long long row_step = (long long)a.q.H * St::kRow;
+  long long tile_l = (long long)split * per + warp;
+  int tile = tile_l < tile_end ? (int)tile_l : tile_end;
+  int slot = tile / tiles_page, in_page = tile - slot * tiles_page, known = -1;
+  const char *kbase = nullptr, *vbase = nullptr;
+  unsigned long long valid_of = 0;  // rows of the tiles asked for, a byte each, the next to be worked on first
+  int asked = 0;
+  auto ask = [&](int stage) {
+    int valid = 0;
+    if (tile < tile_end) {
+      if (slot != known) {
+        known = slot;
+        const int p = a.sel[slot];
+        const bool in = p >= 0 && p < a.NP;
+        kbase = in ? static_cast<const char*>(a.page_k[p]) : nullptr;
+        vbase = in ? static_cast<const char*>(a.page_v[p]) : nullptr;
+        if (!kbase || !vbase || ((reinterpret_cast<uintptr_t>(kbase) | reinterpret_cast<uintptr_t>(vbase)) & 15u)) {
+          kbase = nullptr;
+          set_status(a.status, HSA_ERR_DEVICE);
+        }
+      }
+      if (kbase) {
+        const int row0 = in_page * 16;
+        valid = min((slot < whole ? P : rest) - row0, 16);
+        const uint32_t dst = ring_s + stage * St::kBytes;
+        const long long from = ((long long)row0 * a.q.H + h) * St::kRow + my_vec * 16;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          const int row = my_row + i * (32 / CH);
+          const long long src = from + (row < valid ? row * row_step : 0);
+          cp_async_zero<16>(dst + row * St::kPitch + my_vec * 16, kbase + src, row < valid);
+          cp_async_zero<16>(dst + St::kV + row * St::kPitch + my_vec * 16, vbase + src, row < valid);
+        }
+        const int row = lane & 15;
+        const long long head_row = (long long)(row0 + (row < valid ? row : 0)) * a.q.H + h;
+        cp_async_zero<4 * G>(dst + (lane < 16 ? St::kKs : St::kVs) + row * 4 * G,
+                             (lane < 16 ? kbase : vbase) + a.q.scale_offset + head_row * 4 * G, row < valid);
+      }
+      tile += kAqWarps;
+      for (in_page += kAqWarps; in_page >= tiles_page; in_page -= tiles_page) ++slot;
+    }
+    cp_async_commit();
+    valid_of |= (unsigned long long)valid << (8 * asked);
+    ++asked;
+  };
+  const int rounds = tile < tile_end ? (tile_end - tile + kAqWarps - 1) / kAqWarps : 0;
+#pragma unroll
+  for (int s = 0; s < kAqStages - 1; ++s) ask(s);
 
   // The queries of this tile as product operands: column g of each 8-query tile.
   uint32_t qf[NT][G * KS][2];
@@ -185,15 +266,6 @@ __global__ void __launch_bounds__(kAqThreads) attn_quant_kernel(const AttnQuantA
     qs[n][1] = __shfl_sync(0xffffffffu, unit, 8 * t + 4) * a.scale_log2e;
   }
 
-  // Tiles of the first n rows: tiles_per_page of each whole page, then those of the last one.
-  const long long all = (long long)a.Kp * P;
-  long long n_rows = a.n_rows ? (long long)*a.n_rows : all;
-  n_rows = n_rows < 0 ? 0 : (n_rows > all ? all : n_rows);
-  const int tiles_page = (P + 15) / 16;
-  const long long tiles = n_rows / P * tiles_page + (n_rows % P + 15) / 16;
-  const long long per = (tiles + a.splits - 1) / a.splits;
-  const long long tile_end = min(tiles, (split + 1) * per);
-
   float o[NT][G * KS][4];
   float m[NT][2], l[NT][2];
   float vref[G];
@@ -207,46 +279,32 @@ __global__ void __launch_bounds__(kAqThreads) attn_quant_kernel(const AttnQuantA
 #pragma unroll
   for (int i = 0; i < G; ++i) vref[i] = pow2_below(0.f);
 
-  int known = -1;
-  const char *kbase = nullptr, *vbase = nullptr;
-  const long long row_bytes = (long long)D * BITS / 8;
-  for (long long tile = split * per + warp; tile < tile_end; tile += kAqWarps) {
-    const int slot = (int)(tile / tiles_page);
-    const int row0 = (int)(tile - (long long)slot * tiles_page) * 16;
-    if (slot != known) {
-      known = slot;
-      const int p = a.sel[slot];
-      const bool in = p >= 0 && p < a.NP;
-      kbase = in ? static_cast<const char*>(a.page_k[p]) : nullptr;
-      vbase = in ? static_cast<const char*>(a.page_v[p]) : nullptr;
-      if (!kbase || !vbase || ((reinterpret_cast<uintptr_t>(kbase) | reinterpret_cast<uintptr_t>(vbase)) & 15u)) {
-        kbase = nullptr;
-        set_status(a.status, HSA_ERR_DEVICE);
-      }
-    }
-    if (!kbase) continue;
-    const int valid = (int)min(min((long long)P, n_rows - (long long)slot * P) - row0, 16LL);  // >= 1
-    // loads: keys g and g + 8; values 2t, 2t + 1, 2t + 8, 2t + 9
+  for (int i = 0, stage = 0; i < rounds; ++i, stage = stage == kAqStages - 1 ? 0 : stage + 1) {
+    cp_async_wait<kAqStages - 2>();
+    __syncwarp();  // all lanes' copies are there, and all are done with the stage before
+    const int valid = (int)(valid_of & 255u);
+    valid_of >>= 8;
+    --asked;
+    ask(stage == 0 ? kAqStages - 1 : stage - 1);
+    if (valid == 0) continue;
+    // keys g and g + 8; values 2t, 2t + 1, 2t + 8, 2t + 9
+    const char* st = ring + stage * St::kBytes;
     Raw<KB> kw[2][G];
     Raw<VB> vw[4][G];
     float ks[2][G], vs[2][G];  // scales of rows g and g + 8
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const long long head_row = (long long)(row0 + min(g + 8 * i, valid - 1)) * a.q.H + h;
+    for (int r = 0; r < 2; ++r)
 #pragma unroll
       for (int k = 0; k < G; ++k) {
-        kw[i][k] = load_raw<KB>(kbase + head_row * row_bytes + (k * GROUP + t * (GROUP / 4)) * BITS / 8);
-        ks[i][k] = __ldg(reinterpret_cast<const float*>(kbase + a.q.scale_offset) + head_row * G + k);
-        vs[i][k] = __ldg(reinterpret_cast<const float*>(vbase + a.q.scale_offset) + head_row * G + k);
+        kw[r][k] = read_raw<KB>(st + (g + 8 * r) * St::kPitch + k * GROUP * BITS / 8 + t * KB);
+        ks[r][k] = *reinterpret_cast<const float*>(st + St::kKs + ((g + 8 * r) * G + k) * 4);
+        vs[r][k] = *reinterpret_cast<const float*>(st + St::kVs + ((g + 8 * r) * G + k) * 4);
       }
-    }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const long long head_row = (long long)(row0 + min(2 * t + (i & 1) + 4 * (i & 2), valid - 1)) * a.q.H + h;
+    for (int r = 0; r < 4; ++r)
 #pragma unroll
       for (int k = 0; k < G; ++k)
-        vw[i][k] = load_raw<VB>(vbase + head_row * row_bytes + (k * GROUP + g * (GROUP / 8)) * BITS / 8);
-    }
+        vw[r][k] = read_raw<VB>(st + St::kV + (2 * t + (r & 1) + 4 * (r & 2)) * St::kPitch + k * GROUP * BITS / 8 + g * VB);
     // S = K q
     float s[NT][4];
 #pragma unroll
@@ -345,6 +403,8 @@ __global__ void __launch_bounds__(kAqThreads) attn_quant_kernel(const AttnQuantA
     }
   }
 
+  cp_async_wait<0>();
+  float(*s_o)[D] = reinterpret_cast<float(*)[D]>(ring_all);  // after the barrier below the ring is free
   // Join the warps in order.
 #pragma unroll
   for (int n = 0; n < NT; ++n)
@@ -431,15 +491,21 @@ __global__ void attn_quant_join_kernel(const AttnQuantArgs a, int D) {
   if (d == 0 && a.lse) a.lse[row] = sum == 0.f ? -INFINITY : ref * 0.69314718055994531f + logf(sum);
 }
 
-constexpr int kAqCtasPerSM = 4;
-
 template <int FMT, int D, int GROUP>
 cudaError_t launch(const AttnQuantArgs& a, cudaStream_t s) {
   const int cols = a.T * (a.Hq / a.q.H);
   const unsigned x = (unsigned)(a.q.H * a.splits);
-  if (cols <= 8) attn_quant_kernel<FMT, D, GROUP, 1><<<dim3(x, 1), kAqThreads, 0, s>>>(a);
-  else attn_quant_kernel<FMT, D, GROUP, 2><<<dim3(x, (cols + 15) / 16), kAqThreads, 0, s>>>(a);
-  cudaError_t e = cudaGetLastError();
+  const size_t ring = (size_t)kAqWarps * kAqStages * Stage<FMT, D, GROUP>::kBytes;
+  auto go = [&](auto kernel, int nt) {
+    const size_t join = (size_t)8 * nt * D * sizeof(float), smem = ring > join ? ring : join;
+    if (smem > kDefaultSmemOptIn) {
+      const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (e != cudaSuccess) return e;
+    }
+    kernel<<<dim3(x, (cols + 8 * nt - 1) / (8 * nt)), kAqThreads, smem, s>>>(a);
+    return cudaGetLastError();
+  };
+  cudaError_t e = cols <= 8 ? go(attn_quant_kernel<FMT, D, GROUP, 1>, 1) : go(attn_quant_kernel<FMT, D, GROUP, 2>, 2);
   if (e != cudaSuccess || a.splits == 1) return e;
   const int per = 256 / D;
   const long long rows = (long long)a.T * a.Hq;
@@ -460,14 +526,14 @@ cudaError_t launch_fmt(const AttnQuantArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-// Splits of the rows: about kAqCtasPerSM CTAs on each SM in one wave, at least 4 tiles (one a
+// Splits of the rows: about kAqCtas CTAs on each SM in one wave, at least 4 tiles (one a
 // warp) to a split.
 int attn_quant_splits(int T, int Hq, int H, int d, int Kp, int P_tok) {
   (void)d;
   const int cols = T * (Hq / H);
   const long long tiles = (long long)Kp * ((P_tok + 15) / 16);
   const long long units = (long long)H * (cols <= 8 ? 1 : (cols + 15) / 16);
-  long long n = 148LL * kAqCtasPerSM / units;
+  long long n = 148LL * (cols <= 8 ? kAqCtas : kAqCtasWide) / units;
   const long long most = (tiles + kAqWarps - 1) / kAqWarps;
   if (n > most) n = most;
   return (int)(n < 1 ? 1 : n);

@@ -188,11 +188,10 @@ struct RowsArgs {
   int H;
   long long token_stride, head_stride;
 };
-int rope_head_groups(long long tokens, int J, int heads);
 cudaError_t launch_rope(const RopeArgs& r, int tokens, int d, int dtype, const RowsArgs& q_in, const RowsArgs& q_out,
                         const RowsArgs& k_in, const RowsArgs& k_out, cudaStream_t s);
 
-// ---------------------------------------------------------------- quant.cu
+// ---------------------------------------------------------------- quant_rows.cu / quant_read.cu
 // Quantised pages (layout in include/hsa.h).
 struct QuantArgs {
   int format, group;

@@ -1,0 +1,286 @@
+// Selected quantised pages read back into the contiguous bf16 active cache, with the keys
+// rotated to their places there and their 128-row block means taken in the same pass.
+//
+// HBM bound, two thirds and more of it writes: 1 or 1/2 byte read and 2 written an element.
+// What counts beside enough loads in flight is that the CTAs which run at one time write
+// neighbouring memory: 16-row CTAs (a window of some 70 MB, all of it written from end to
+// end) reach 95% of the copy rate without a rotation, where CTAs of 128 rows, each on a
+// stretch of its own, stay at 85%.
+#include "common.cuh"
+#include "kernels.h"
+#include "quant.cuh"
+#include "rope.cuh"
+
+namespace hsa {
+namespace {
+
+// A CTA takes 16 rows of V, or of K, and a slab of heads: thread (item, phase) owns the two
+// chunks `item` of every row phase, phase + phases, ...  With the block means it takes 128
+// rows of K instead (a cluster of eight 16-row CTAs that added up their sums took 35%
+// longer, and smaller slabs compute more cos and sin: 20 heads to a slab 7% longer than
+// 40).  The cos and sin of 32 rows at a time are computed
+// into shared memory (all heads of the slab use them).  The block means are summed a thread's
+// rows first, then phase by phase in order (deterministic).
+constexpr int kReadCtas = 3;  // on an SM
+constexpr int kReadRing = 4;
+constexpr int kReadThreads = 320;
+constexpr int kReadRows = 16;
+constexpr int kReadBatch = 32;  // rows whose cos and sin are held at once
+
+struct ReadArgs {
+  QuantArgs q;
+  RopeArgs r;
+  const void* const* page_k;
+  const void* const* page_v;
+  int NP;
+  const int32_t* sel;
+  long long Lc;
+  struct Part {        // how K's, or V's, rows are shared out to CTAs
+    int slab, slabs;   // heads of a CTA, and how many such slabs there are (the fastest index)
+    int phases;
+    unsigned ctas;
+  } k, v;
+  int ring_offset;
+  uint16_t* Kc;
+  uint16_t* Vc;
+  float* kbar128;
+  int* status;
+};
+
+// A thread's way through its rows phase, phase + phases, ... of a CTA: where the next one's
+// codes and scales are.
+template <int FMT, int J>
+struct ReadCursor {
+  const char* codes;
+  const float* scales;
+  long long code_step, scale_step;
+  int row;         // next row
+  int left;        // rows from there to its page's end
+  int slot, phases;
+
+  __device__ __forceinline__ void seek(const ReadArgs& a, const void* const* table, long long r0, int h) {
+    constexpr int D = 16 * J;
+    slot = (int)((r0 + row) / a.q.P_tok);
+    const int t = (int)(r0 + row - (long long)slot * a.q.P_tok);
+    left = a.q.P_tok - t;
+    const int p = a.sel[slot];
+    const char* base = (p >= 0 && p < a.NP) ? static_cast<const char*>(table[p]) : nullptr;
+    codes = nullptr;
+    if (base == nullptr || (reinterpret_cast<uintptr_t>(base) & 15u) != 0) {
+      set_status(a.status, HSA_ERR_DEVICE);
+    } else {
+      const long long head_row = (long long)t * a.q.H + h;
+      codes = base + head_row * (D * code_bits<FMT>() / 8);
+      scales = reinterpret_cast<const float*>(base + a.q.scale_offset) + head_row * (D / a.q.group);
+    }
+  }
+  // The step to the next row; false at the CTA's end.
+  __device__ __forceinline__ bool next(const ReadArgs& a, const void* const* table, long long r0, int h, int rows) {
+    row += phases;
+    if (row >= rows) return false;
+    left -= phases;
+    if (left > 0) {
+      if (codes) {
+        codes += code_step;
+        scales += scale_step;
+      }
+    } else {
+      seek(a, table, r0, h);
+    }
+    return true;
+  }
+};
+
+// A thread's own ring in shared memory: its codes and scales of the next kReadRing - 1
+// rounds are on their way while it works on one, at no cost in registers.  A slot is filled
+// again one round after it was read.
+template <int FMT>
+struct ReadSlot {
+  static constexpr int kCodeBytes = code_bits<FMT>();  // of 8 columns
+  static constexpr int kBytes = 2 * kCodeBytes + 8;    // lo and hi chunk, their two scales
+};
+
+template <int FMT, int J, int ROPE, bool POOL, int ROWS>
+__device__ __forceinline__ void read_rows(const ReadArgs& a, const ReadArgs::Part& part, unsigned cta,
+                                          const void* const* table, uint16_t* dst, float* smem) {
+  constexpr int D = 16 * J, BITS = code_bits<FMT>();
+  const QuantArgs& q = a.q;
+  const long long blk = cta / part.slabs, r0 = blk * ROWS;
+  const int rows = (int)min((long long)ROWS, a.Lc - r0);
+  const int h0 = (int)(cta - blk * part.slabs) * part.slab;
+  const int items = min(part.slab, q.H - h0) * J, phases = part.phases;
+  const int tid = threadIdx.x;
+  const int phase = tid / (part.slab * J), item = tid - phase * (part.slab * J);
+  const int j = item % J, h = h0 + item / J;
+  const bool active = phase < phases && item < items;
+  const ChunkPair c = chunk_pair<J, ROPE>(a.r, j);
+  const int lo_group = c.lo * 8 / q.group, hi_group = c.hi * 8 / q.group;
+  float acc[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) acc[k] = 0.f;
+  ReadCursor<FMT, J> at;
+  at.phases = phases;
+  at.code_step = (long long)phases * q.H * (D * BITS / 8);
+  at.scale_step = (long long)phases * q.H * (D / q.group);
+  at.row = phase;
+  bool more = active && phase < rows;
+  if (more) at.seek(a, table, r0, h);
+  // the ring lies behind the cos and sin: lo codes, hi codes, scales, each [slot][thread]
+  constexpr int CB = ReadSlot<FMT>::kCodeBytes;
+  const int threads = blockDim.x;
+  char* ring = reinterpret_cast<char*>(smem) + a.ring_offset;
+  char* ring_lo = ring + tid * CB;
+  char* ring_hi = ring_lo + kReadRing * threads * CB;
+  char* ring_s = ring + 2 * kReadRing * threads * CB + tid * 8;
+  const uint32_t dst_lo = smem_u32(ring_lo), dst_hi = smem_u32(ring_hi), dst_s = smem_u32(ring_s);
+  uint32_t there = 0;  // bit s: slot s holds a row
+  auto ask = [&](int slot) {
+    there &= ~(1u << slot);
+    if (more) {
+      if (at.codes) {
+        there |= 1u << slot;
+        cp_async<CB>(dst_lo + slot * threads * CB, at.codes + c.lo * BITS);
+        cp_async<CB>(dst_hi + slot * threads * CB, at.codes + c.hi * BITS);
+        cp_async<4>(dst_s + slot * threads * 8, at.scales + lo_group);
+        cp_async<4>(dst_s + slot * threads * 8 + 4, at.scales + hi_group);
+      }
+      more = at.next(a, table, r0, h, rows);
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < kReadRing - 1; ++s) ask(s);
+  uint16_t* out = dst + ((r0 + phase) * q.H + h) * D;
+  const long long out_step = (long long)phases * q.H * D;
+  int slot = 0, i = phase;
+  for (int b0 = 0; b0 < rows; b0 += kReadBatch) {
+    if constexpr (ROPE != kRopeNone) {
+      if (ROWS > kReadBatch && b0) __syncthreads();  // the last rows' cos and sin have been read
+      rope_table<J, ROPE>(a.r, r0 + b0, min(kReadBatch, rows - b0), reinterpret_cast<float4*>(smem), tid, threads);
+      __syncthreads();
+    }
+    const int end = active ? min(rows, b0 + kReadBatch) : 0;
+    for (; i < end; i += phases) {
+      ask(slot == 0 ? kReadRing - 1 : slot - 1);
+      cp_async_wait<kReadRing - 1>();
+      if (there >> slot & 1) {
+        Codes8<FMT> lo, hi;
+        if constexpr (FMT == HKV_QUANT_INT4) {
+          lo.w[0] = *reinterpret_cast<const uint32_t*>(ring_lo + slot * threads * CB);
+          hi.w[0] = *reinterpret_cast<const uint32_t*>(ring_hi + slot * threads * CB);
+        } else {
+          const uint2 u = *reinterpret_cast<const uint2*>(ring_lo + slot * threads * CB);
+          const uint2 v = *reinterpret_cast<const uint2*>(ring_hi + slot * threads * CB);
+          lo.w[0] = u.x; lo.w[1] = u.y;
+          hi.w[0] = v.x; hi.w[1] = v.y;
+        }
+        const float2 s = *reinterpret_cast<const float2*>(ring_s + slot * threads * 8);
+        float x[8], y[8];
+        decode8<FMT>(lo, s.x, x);
+        decode8<FMT>(hi, s.y, y);
+        rotate_chunks<J, ROPE>(c, reinterpret_cast<const float4*>(smem) + (i - b0) * 4 * J, j, x, y);
+        if constexpr (POOL) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            acc[k] += x[k];
+            acc[8 + k] += y[k];
+          }
+        }
+        Chunk<__nv_bfloat16> w;
+        w.set(x);
+        w.store(out + c.lo * 8);
+        w.set(y);
+        w.store(out + c.hi * 8);
+      }
+      out += out_step;
+      slot = slot == kReadRing - 1 ? 0 : slot + 1;
+    }
+  }
+  cp_async_wait<0>();
+  if constexpr (POOL) {
+    __syncthreads();  // the last cos and sin have been read
+    for (int p = 0; p < phases; ++p) {
+      if (active && phase == p) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          float& s = smem[(item / J) * D + (k < 8 ? c.lo * 8 + k : c.hi * 8 + k - 8)];
+          s = p == 0 ? acc[k] : s + acc[k];
+        }
+      }
+      __syncthreads();
+    }
+    const float inv = 1.f / (float)rows;
+    float* mean = a.kbar128 + (blk * q.H + h0) * D;
+    for (int v = tid; v < items / J * D; v += threads) mean[v] = smem[v] * inv;
+  }
+}
+
+template <int FMT, int J, int ROPE, bool POOL>
+__global__ void __launch_bounds__(kReadThreads, kReadCtas) gather_quant_kernel(const ReadArgs a) {
+  extern __shared__ __align__(16) float smem[];
+  if (blockIdx.x < a.k.ctas)
+    read_rows<FMT, J, ROPE, POOL, POOL ? 128 : kReadRows>(a, a.k, blockIdx.x, a.page_k, a.Kc, smem);
+  else
+    read_rows<FMT, J, kRopeNone, false, kReadRows>(a, a.v, blockIdx.x - a.k.ctas, a.page_v, a.Vc, smem);
+}
+
+// The shares of CTAs of `rows` rows.
+template <int J>
+ReadArgs::Part read_part(const ReadArgs& a, int rows) {
+  ReadArgs::Part p;
+  p.slabs = (a.q.H * J + kReadThreads - 1) / kReadThreads;
+  p.slab = (a.q.H + p.slabs - 1) / p.slabs;
+  p.slabs = (a.q.H + p.slab - 1) / p.slab;
+  p.phases = kReadThreads / (p.slab * J);
+  if (p.phases > rows) p.phases = rows;
+  p.ctas = (unsigned)((a.Lc + rows - 1) / rows * p.slabs);
+  return p;
+}
+
+template <int FMT, int J, int ROPE, bool POOL>
+cudaError_t launch_read(ReadArgs& a, cudaStream_t s) {
+  a.k = read_part<J>(a, POOL ? 128 : kReadRows);
+  a.v = read_part<J>(a, kReadRows);
+  const int need = max(a.k.slab * a.k.phases, a.v.slab * a.v.phases) * J;
+  const int threads = max(8 * J, (need + 31) / 32 * 32);  // 8 J: the cos and sin of a row
+  size_t smem = ROPE != kRopeNone ? (size_t)(POOL ? kReadBatch : kReadRows) * 8 * J * sizeof(float2) : 0;
+  const size_t pool = POOL ? (size_t)a.k.slab * J * 16 * sizeof(float) : 0;
+  if (pool > smem) smem = pool;
+  a.ring_offset = (int)smem;
+  smem += (size_t)kReadRing * threads * ReadSlot<FMT>::kBytes;
+  if (smem > kDefaultSmemOptIn) {
+    const cudaError_t e = cudaFuncSetAttribute(gather_quant_kernel<FMT, J, ROPE, POOL>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  gather_quant_kernel<FMT, J, ROPE, POOL><<<a.k.ctas + a.v.ctas, threads, smem, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <int FMT, int J>
+cudaError_t launch_read_rope(ReadArgs& a, cudaStream_t s) {
+  if (!a.r.on) return a.kbar128 ? launch_read<FMT, J, kRopeNone, true>(a, s) : launch_read<FMT, J, kRopeNone, false>(a, s);
+  if (a.r.half_layout)
+    return a.kbar128 ? launch_read<FMT, J, kRopeHalf, true>(a, s) : launch_read<FMT, J, kRopeHalf, false>(a, s);
+  return a.kbar128 ? launch_read<FMT, J, kRopeInterleaved, true>(a, s) : launch_read<FMT, J, kRopeInterleaved, false>(a, s);
+}
+
+template <int FMT>
+cudaError_t launch_read_head(ReadArgs& a, cudaStream_t s) {
+  return a.q.d == 128 ? launch_read_rope<FMT, 8>(a, s) : launch_read_rope<FMT, 4>(a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_gather_quant(const QuantArgs& q, const RopeArgs& r, const void* const* page_k,
+                                const void* const* page_v, int NP, const int32_t* sel, int Kp, uint16_t* Kc,
+                                uint16_t* Vc, float* kbar128, int* status, cudaStream_t s) {
+  ReadArgs a{q, r, page_k, page_v, NP, sel, (long long)Kp * q.P_tok, {}, {}, 0, Kc, Vc, kbar128, status};
+  switch (q.format) {
+    case HKV_QUANT_E4M3: return launch_read_head<HKV_QUANT_E4M3>(a, s);
+    case HKV_QUANT_INT8: return launch_read_head<HKV_QUANT_INT8>(a, s);
+    default: return launch_read_head<HKV_QUANT_INT4>(a, s);
+  }
+}
+
+}  // namespace hsa

@@ -1,10 +1,9 @@
 // Rotary positions of queries and keys (forward, and backward with the angle's sign
 // turned): y = mscale R(theta) x, one read and one write of every element.
 //
-// HBM bound: 2 x size bytes and 3 FLOP an element.  A thread keeps the cos and sin of its
-// eight pairs in registers and walks over a share of the token's heads (queries, then
-// keys), so an angle is computed once per share and not once per head, and nothing is
-// written to or read from a table.
+// HBM bound: 2 x size bytes and 3 FLOP an element.  A CTA takes a few tokens with all their
+// heads (queries, then keys).  Its threads first ask for their elements, then compute the
+// tokens' cos and sin into shared memory while those are on the way.
 #include "common.cuh"
 #include "kernels.h"
 #include "rope.cuh"
@@ -12,87 +11,101 @@
 namespace hsa {
 namespace {
 
-constexpr int kRopeThreads = 128;
-constexpr int kRopeUnroll = 4;  // heads in flight a thread
+constexpr int kRopeThreads = 256;
+constexpr int kRopeCtas = 6;      // on an SM: that many threads' loads hide the latency, one unit each
+constexpr int kRopeRounds = 5;
+constexpr int kRopeMaxRows = 32;  // tokens of a CTA (16 KB of cos and sin at d = 128)
 
-template <typename T>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs r, long long tokens, int J, int groups,
-                                                            const RowsArgs qi, const RowsArgs qo, const RowsArgs ki,
-                                                            const RowsArgs ko) {
-  const long long item = (long long)blockIdx.x * kRopeThreads + threadIdx.x;
-  const int j = (int)(item % J);
-  const long long rest = item / J;
-  const int g = (int)(rest % groups);
-  const long long t = rest / groups;
-  if (t >= tokens) return;
-  const ChunkPair c = chunk_pair(r, j, J);
-  float2 cs[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    cs[i] = (i < 4 ? c.rot_lo : c.rot_hi) ? rope_cos_sin(r, t, slot_pair(r, c, i)) : make_float2(1.f, 0.f);
-  const int heads = qi.H + ki.H;
-  const T* qsrc = static_cast<const T*>(qi.data) + t * qi.token_stride;
-  const T* ksrc = static_cast<const T*>(ki.data) + t * ki.token_stride;
-  T* qdst = static_cast<T*>(qo.data) + t * qo.token_stride;
-  T* kdst = static_cast<T*>(ko.data) + t * ko.token_stride;
-  for (int h0 = g; h0 < heads; h0 += groups * kRopeUnroll) {
-    Chunk<T> lo[kRopeUnroll], hi[kRopeUnroll];
-#pragma unroll
-    for (int u = 0; u < kRopeUnroll; ++u) {
-      const int h = h0 + u * groups;
-      if (h < heads) {
-        const T* src = h < qi.H ? qsrc + h * qi.head_stride : ksrc + (h - qi.H) * ki.head_stride;
-        lo[u].load(src + c.lo * 8);
-        hi[u].load(src + c.hi * 8);
-      }
+template <typename T, int J, int ROPE>
+__global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(const RopeArgs r, int tokens, int rows_per_cta,
+                                                                       int slab, const RowsArgs qi, const RowsArgs qo,
+                                                                       const RowsArgs ki, const RowsArgs ko) {
+  extern __shared__ float4 table[];
+  const int tid = threadIdx.x, j = tid % J;
+  const long long t0 = (long long)blockIdx.x * rows_per_cta;
+  const int rows = (int)min((long long)rows_per_cta, tokens - t0);
+  const int h0 = blockIdx.y * slab;
+  const int heads = min(slab, qi.H + ki.H - h0);
+  const ChunkPair c = chunk_pair<J, ROPE>(r, j);
+  constexpr int kUnits = kRopeThreads / J;  // (token, head) units of a round, J threads each
+  int row = tid / J / heads, head = tid / J % heads;
+  bool first = true;
+  while (first || row < rows) {
+    Chunk<T> lo, hi;
+    T* dst = nullptr;
+    if (row < rows) {
+      const int h = h0 + head;
+      const bool is_q = h < qi.H;
+      const RowsArgs& in = is_q ? qi : ki;
+      const RowsArgs& out = is_q ? qo : ko;
+      const int hh = is_q ? h : h - qi.H;
+      const T* src = static_cast<const T*>(in.data) + (t0 + row) * in.token_stride + hh * in.head_stride;
+      dst = static_cast<T*>(out.data) + (t0 + row) * out.token_stride + hh * out.head_stride;
+      lo.load(src + c.lo * 8);
+      hi.load(src + c.hi * 8);
     }
-#pragma unroll
-    for (int u = 0; u < kRopeUnroll; ++u) {
-      const int h = h0 + u * groups;
-      if (h < heads) {
-        T* dst = h < qi.H ? qdst + h * qo.head_stride : kdst + (h - qi.H) * ko.head_stride;
-        if (c.rot_lo || c.rot_hi) {
-          float a[8], b[8];
-          lo[u].get(a);
-          hi[u].get(b);
-          rotate_chunks(r, c, cs, a, b);
-          if (c.rot_lo) lo[u].set(a);
-          if (c.rot_hi) hi[u].set(b);
-        }
-        lo[u].store(dst + c.lo * 8);
-        hi[u].store(dst + c.hi * 8);
-      }
+    if (first) {  // every thread comes here once
+      rope_table<J, ROPE>(r, t0, rows, table, tid, kRopeThreads);
+      __syncthreads();
+      first = false;
     }
+    if (row < rows) {
+      if (c.rot_lo || c.rot_hi) {
+        float a[8], b[8];
+        lo.get(a);
+        hi.get(b);
+        rotate_chunks<J, ROPE>(c, table + row * 4 * J, j, a, b);
+        if (c.rot_lo) lo.set(a);
+        if (c.rot_hi) hi.set(b);
+      }
+      lo.store(dst + c.lo * 8);
+      hi.store(dst + c.hi * 8);
+    }
+    for (head += kUnits; head >= heads; head -= heads) ++row;
   }
 }
 
-template <typename T>
-cudaError_t launch(const RopeArgs& r, int tokens, int d, const RowsArgs& qi, const RowsArgs& qo, const RowsArgs& ki,
+template <typename T, int J, int ROPE>
+cudaError_t launch(const RopeArgs& r, int tokens, const RowsArgs& qi, const RowsArgs& qo, const RowsArgs& ki,
                    const RowsArgs& ko, cudaStream_t s) {
-  const int J = d / 16, heads = qi.H + ki.H;
-  const int groups = rope_head_groups(tokens, J, heads);
-  const long long items = (long long)tokens * groups * J;
-  rope_kernel<T><<<(unsigned)((items + kRopeThreads - 1) / kRopeThreads), kRopeThreads, 0, s>>>(r, tokens, J, groups, qi,
-                                                                                             qo, ki, ko);
+  const int heads = qi.H + ki.H;
+  // Tokens of a CTA: where there are CTAs enough for every SM, of those that its threads get
+  // through in kRopeRounds rounds the number that leaves the fewest of them idle in the last
+  // one.  Its heads are shared out as well while that leaves SMs idle.
+  int rows = 1, best = 0;
+  const int most = tokens / (148 * kRopeCtas);
+  for (int n = 1; n == 1 || (n <= kRopeMaxRows && n <= most); ++n) {
+    const int rounds = (n * heads + kRopeThreads / J - 1) / (kRopeThreads / J);
+    const int used = n * heads * 100 / (rounds * (kRopeThreads / J));
+    if (n > 1 && rounds > kRopeRounds) break;
+    if (used > best) rows = n, best = used;
+  }
+  const long long ctas = ((long long)tokens + rows - 1) / rows;
+  int slab = heads;
+  while (slab > kRopeThreads / J && ctas * ((heads + slab - 1) / slab) < 148) slab = (slab + 1) / 2;
+  rope_kernel<T, J, ROPE><<<dim3((unsigned)ctas, (heads + slab - 1) / slab), kRopeThreads,
+                            (size_t)rows * 8 * J * sizeof(float2), s>>>(r, tokens, rows, slab, qi, qo, ki, ko);
   return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_type(const RopeArgs& r, int tokens, int d, const RowsArgs& qi, const RowsArgs& qo, const RowsArgs& ki,
+                        const RowsArgs& ko, cudaStream_t s) {
+  if (d == 128)
+    return r.half_layout ? launch<T, 8, kRopeHalf>(r, tokens, qi, qo, ki, ko, s)
+                         : launch<T, 8, kRopeInterleaved>(r, tokens, qi, qo, ki, ko, s);
+  return r.half_layout ? launch<T, 4, kRopeHalf>(r, tokens, qi, qo, ki, ko, s)
+                       : launch<T, 4, kRopeInterleaved>(r, tokens, qi, qo, ki, ko, s);
 }
 
 }  // namespace
 
-// Shares that a token's heads are cut into: as many as it takes to have about 2048 threads
-// on each SM, at most one a head.  Fewer shares compute fewer angles, more shares keep more
-// loads in flight.
-int rope_head_groups(long long tokens, int J, int heads) {
-  const long long want = (148LL * 2048 + tokens * J - 1) / (tokens * J);
-  return (int)(want < 1 ? 1 : (want > heads ? heads : want));
-}
-
 cudaError_t launch_rope(const RopeArgs& r, int tokens, int d, int dtype, const RowsArgs& qi, const RowsArgs& qo,
                         const RowsArgs& ki, const RowsArgs& ko, cudaStream_t s) {
   switch (dtype) {
-    case HSA_DTYPE_BF16: return launch<__nv_bfloat16>(r, tokens, d, qi, qo, ki, ko, s);
-    case HSA_DTYPE_FP16: return launch<__half>(r, tokens, d, qi, qo, ki, ko, s);
-    default: return launch<float>(r, tokens, d, qi, qo, ki, ko, s);
+    case HSA_DTYPE_BF16: return launch_type<__nv_bfloat16>(r, tokens, d, qi, qo, ki, ko, s);
+    case HSA_DTYPE_FP16: return launch_type<__half>(r, tokens, d, qi, qo, ki, ko, s);
+    default: return launch_type<float>(r, tokens, d, qi, qo, ki, ko, s);
   }
 }
 

@@ -2,12 +2,14 @@
 // write into quantised pages and the read back from them.
 //
 // A thread works on two 8-column chunks of one (row, head), `lo` and `hi`, chosen so that
-// both members of each of its eight pairs are its own: thread j of a head's d / 16 has
-//   interleaved  chunks j and j + d/16; pairs 4 lo .. 4 lo + 3, then 4 hi .. 4 hi + 3
+// both members of each of its eight pairs are its own: thread j of a head's J = d / 16 has
+//   interleaved  chunks j and j + J; pairs 4 lo .. 4 lo + 3, then 4 hi .. 4 hi + 3
 //   half         while j < rot/16: chunks j and j + rot/16, pairs 8 j .. 8 j + 7;
 //                above: two neighbouring chunks behind the rotated columns
 // so that a row is rotated in registers, with no exchange between threads, and every
 // access is a whole 16-byte (bf16, fp16), 32-byte (fp32) or 8 / 4-byte (codes) vector.
+// The cos and sin of a row's pairs are computed once a CTA, into shared memory, and used
+// for all of the row's heads there.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -17,14 +19,19 @@
 
 namespace hsa {
 
+constexpr int kRopeNone = 0;
+constexpr int kRopeInterleaved = 1;
+constexpr int kRopeHalf = 2;
+
 struct ChunkPair {
-  int lo, hi;        // 8-column chunks of the head
-  bool rot_lo, rot_hi;
+  int lo, hi;           // 8-column chunks of the head
+  bool rot_lo, rot_hi;  // whether they are rotated
 };
 
-__device__ __forceinline__ ChunkPair chunk_pair(const RopeArgs& r, int j, int J) {
+template <int J, int ROPE>
+__device__ __forceinline__ ChunkPair chunk_pair(const RopeArgs& r, int j) {
   ChunkPair c;
-  if (r.on && r.half_layout) {
+  if constexpr (ROPE == kRopeHalf) {
     const int rh = r.pairs / 8;  // chunks in each half of the rotated columns
     const bool in = j < rh;
     c.lo = in ? j : 2 * rh + 2 * (j - rh);
@@ -33,58 +40,72 @@ __device__ __forceinline__ ChunkPair chunk_pair(const RopeArgs& r, int j, int J)
   } else {
     c.lo = j;
     c.hi = j + J;
-    c.rot_lo = r.on && c.lo * 4 < r.pairs;
-    c.rot_hi = r.on && c.hi * 4 < r.pairs;
+    c.rot_lo = ROPE == kRopeInterleaved && c.lo * 4 < r.pairs;
+    c.rot_hi = ROPE == kRopeInterleaved && c.hi * 4 < r.pairs;
   }
   return c;
 }
 
-// The pair that slot i (0..7) of a thread's two chunks belongs to (only for rotated ones).
-__device__ __forceinline__ int slot_pair(const RopeArgs& r, const ChunkPair& c, int i) {
-  return r.half_layout ? 8 * c.lo + i : 4 * (i < 4 ? c.lo : c.hi) + (i & 3);
-}
-
-// (mscale cos, mscale sin) of pair p at token t.  The angle in turns, pos * inv_freq / 2 pi,
+// (mscale cos, mscale sin) of a pair at a position.  The angle in turns, pos * inv_freq / 2 pi,
 // is formed and reduced to [-1/2, 1/2] in fp64: its error is about 2^-52 of the turns made
 // (2^-21 of a turn after 2^31 of them), and the fp32 rounding behind the reduction costs at
 // most 2^-26 of a turn.  sign = -1 turns backward (the gradient).
-__device__ __forceinline__ float2 rope_cos_sin(const RopeArgs& r, long long t, int p) {
-  const int axis = (p >= r.end0) + (p >= r.end1);
-  const double pos = (double)r.pos[axis * r.pos_stride + t];
-  double turns = pos * (r.inv_freq[p] * 0.15915494309189533577);  // 1 / (2 pi)
+__device__ __forceinline__ float2 rope_cos_sin(const RopeArgs& r, int pos, double turns_per_step) {
+  double turns = (double)pos * turns_per_step;
   turns -= rint(turns);
   float s, c;
   sincospif((float)(2.0 * turns), &s, &c);
   return make_float2(c * r.mscale, s * r.mscale * r.sign);
 }
 
-// Rotate a thread's two chunks in fp32; cs[i]: cos and sin of slot i.
-__device__ __forceinline__ void rotate_chunks(const RopeArgs& r, const ChunkPair& c, const float2* cs, float* lo,
-                                              float* hi) {
-  if (r.half_layout) {
+// The cos and sin of `rows` tokens from t0 on, in the order the threads read them: for each
+// row four planes, plane k holding slots 2k and 2k + 1 of each of the row's J threads, so that
+// the J threads' 16-byte reads of a plane are contiguous.  Slots of chunks that are not
+// rotated are left out.
+template <int J, int ROPE>
+__device__ __forceinline__ void rope_table(const RopeArgs& r, long long t0, int rows, float4* table, int tid,
+                                           int threads) {
+  // a thread keeps its slot (and so its pair) and walks over rows; threads >= 8 J
+  const int rows_at_once = threads / (8 * J), slot = tid % (8 * J);
+  const int plane = slot / (2 * J), j = slot % (2 * J) / 2, i = 2 * plane + (slot & 1);
+  const ChunkPair c = chunk_pair<J, ROPE>(r, j);
+  if (tid >= rows_at_once * 8 * J || !(i < 4 ? c.rot_lo : c.rot_hi)) return;
+  const int p = ROPE == kRopeHalf ? 8 * c.lo + i : 4 * (i < 4 ? c.lo : c.hi) + (i & 3);
+  const int32_t* pos = r.pos + ((p >= r.end0) + (p >= r.end1)) * r.pos_stride + t0;
+  const double turns_per_step = __ldg(r.inv_freq + p) * 0.15915494309189533577;  // 1 / (2 pi)
+  for (int row = tid / (8 * J); row < rows; row += rows_at_once)
+    reinterpret_cast<float2*>(table)[row * 8 * J + slot] = rope_cos_sin(r, __ldg(pos + row), turns_per_step);
+}
+
+// Rotate a thread's two chunks in fp32; row: the table's row of its token.
+template <int J, int ROPE>
+__device__ __forceinline__ void rotate_chunks(const ChunkPair& c, const float4* row, int j, float* lo, float* hi) {
+  if constexpr (ROPE == kRopeHalf) {
     if (c.rot_lo) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float a = lo[i], b = hi[i];
-        lo[i] = a * cs[i].x - b * cs[i].y;
-        hi[i] = b * cs[i].x + a * cs[i].y;
+      for (int k = 0; k < 4; ++k) {
+        const float4 v = row[k * J + j];
+        const float a0 = lo[2 * k], b0 = hi[2 * k], a1 = lo[2 * k + 1], b1 = hi[2 * k + 1];
+        lo[2 * k] = a0 * v.x - b0 * v.y;
+        hi[2 * k] = b0 * v.x + a0 * v.y;
+        lo[2 * k + 1] = a1 * v.z - b1 * v.w;
+        hi[2 * k + 1] = b1 * v.z + a1 * v.w;
       }
     }
-  } else {
-    if (c.rot_lo) {
+  } else if constexpr (ROPE == kRopeInterleaved) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float a = lo[2 * i], b = lo[2 * i + 1];
-        lo[2 * i] = a * cs[i].x - b * cs[i].y;
-        lo[2 * i + 1] = b * cs[i].x + a * cs[i].y;
-      }
-    }
-    if (c.rot_hi) {
+    for (int half = 0; half < 2; ++half) {
+      float* x = half ? hi : lo;
+      if (half ? c.rot_hi : c.rot_lo) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float a = hi[2 * i], b = hi[2 * i + 1];
-        hi[2 * i] = a * cs[4 + i].x - b * cs[4 + i].y;
-        hi[2 * i + 1] = b * cs[4 + i].x + a * cs[4 + i].y;
+        for (int k = 0; k < 2; ++k) {
+          const float4 v = row[(2 * half + k) * J + j];
+          const float a0 = x[4 * k], b0 = x[4 * k + 1], a1 = x[4 * k + 2], b1 = x[4 * k + 3];
+          x[4 * k] = a0 * v.x - b0 * v.y;
+          x[4 * k + 1] = b0 * v.x + a0 * v.y;
+          x[4 * k + 2] = a1 * v.z - b1 * v.w;
+          x[4 * k + 3] = b1 * v.z + a1 * v.w;
+        }
       }
     }
   }
@@ -98,6 +119,7 @@ template <>
 struct Chunk<__nv_bfloat16> {
   uint4 v;
   __device__ __forceinline__ void load(const void* p) { v = *static_cast<const uint4*>(p); }
+  __device__ __forceinline__ void load_split(const void* p, int) { load(p); }
   __device__ __forceinline__ void store(void* p) const { *static_cast<uint4*>(p) = v; }
   __device__ __forceinline__ void get(float* f) const {
     f[0] = bf16_lo(v.x); f[1] = bf16_hi(v.x); f[2] = bf16_lo(v.y); f[3] = bf16_hi(v.y);
@@ -112,6 +134,7 @@ template <>
 struct Chunk<__half> {
   uint4 v;
   __device__ __forceinline__ void load(const void* p) { v = *static_cast<const uint4*>(p); }
+  __device__ __forceinline__ void load_split(const void* p, int) { load(p); }
   __device__ __forceinline__ void store(void* p) const { *static_cast<uint4*>(p) = v; }
   __device__ __forceinline__ void get(float* f) const {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -139,6 +162,11 @@ struct Chunk<float> {
   __device__ __forceinline__ void load(const void* p) {
     a = static_cast<const float4*>(p)[0];
     b = static_cast<const float4*>(p)[1];
+  }
+  // its two 16-byte vectors `step` bytes apart
+  __device__ __forceinline__ void load_split(const void* p, int step) {
+    a = *static_cast<const float4*>(p);
+    b = *reinterpret_cast<const float4*>(static_cast<const char*>(p) + step);
   }
   __device__ __forceinline__ void store(void* p) const {
     static_cast<float4*>(p)[0] = a;
