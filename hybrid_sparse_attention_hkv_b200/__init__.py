@@ -487,14 +487,23 @@ def _rows(t, what, where, device, dtype, T, d):
     return _Rows(t.data_ptr(), shape[1], step, head)
 
 
-def _on_device(device, call):
-    """call() with `device` current (the launch goes to the tensors' device)."""
+def _launch(where, device, stream, fn, *args):
+    """fn(*args, stream) with `device` current: on `stream`, or on the device's current one."""
     if device.type != "cuda":
-        raise HsaError(1, "device", f"the tensors are on {device}, not on a CUDA device")
+        _refuse(where, f"the tensors are on {device}, not on a CUDA device")
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(device.index)  # torch.cuda.current_stream takes 3 us more
+    elif stream.device != device:
+        _refuse(where, f"the stream is on {stream.device}, not on {device}")
+    else:
+        raw = stream.cuda_stream
     if device.index == torch.cuda.current_device():
-        return call()
-    with torch.cuda.device(device):
-        return call()
+        code = fn(*args, raw)
+    else:
+        with torch.cuda.device(device):
+            code = fn(*args, raw)
+    if code != 0:
+        _check(code, where)
 
 
 class Rope:
@@ -553,9 +562,8 @@ def _rope_call(name, rope, pos, q, q_out, k, k_out, stream):
         ki = ctypes.byref(_rows(k, "k", name, device, dtype, T, d))
         ko = ctypes.byref(_rows(k_out, "k_out", name, device, dtype, T, d))
     r, at, step = _positions(rope, pos, name, device, T)
-    fn = getattr(load_library(), name)
-    _on_device(device, lambda: _check(fn(r, at, step, T, d, _DTYPES[dtype], ctypes.byref(qi), ctypes.byref(qo), ki, ko,
-                                         _stream(stream)), name))
+    _launch(name, device, stream, getattr(load_library(), name), r, at, step, T, d, _DTYPES[dtype], ctypes.byref(qi),
+            ctypes.byref(qo), ki, ko)
 
 
 def hsa_rope(rope, pos, q, q_out, k=None, k_out=None, stream=None):
@@ -602,9 +610,8 @@ def hkv_quant_rows(quant: Quant, K, V, page_k_ptrs, page_v_ptrs, P_tok, first_ro
     dev = None
     if first_row_dev is not None:
         dev = _tensor(first_row_dev.view(-1), "first_row_dev", where, device, torch.int64, (1,))
-    _on_device(device, lambda: _check(load_library().hkv_quant_rows(
-        ctypes.byref(quant), ctypes.byref(k), ctypes.byref(v), T, d, _DTYPES[dtype], r, at, step, pk, pv, NP, P_tok, first_row,
-        dev, w, wn, _stream(stream)), where))
+    _launch(where, device, stream, load_library().hkv_quant_rows, ctypes.byref(quant), ctypes.byref(k), ctypes.byref(v), T, d,
+            _DTYPES[dtype], r, at, step, pk, pv, NP, P_tok, first_row, dev, w, wn)
 
 
 def hkv_gather_quant(quant: Quant, page_k_ptrs, page_v_ptrs, sel, Kp, P_tok, H, d, Kc, Vc, ws, kbar128=None, rope=None,
@@ -618,8 +625,8 @@ def hkv_gather_quant(quant: Quant, page_k_ptrs, page_v_ptrs, sel, Kp, P_tok, H, 
     vc = _tensor(Vc, "Vc", where, device, torch.bfloat16, (Lc, H, d))
     kb = None if kbar128 is None else _tensor(kbar128, "kbar128", where, device, torch.float32, (-(-Lc // 128), H, d))
     r, at, step = _positions(rope, pos, where, device, Lc)
-    _on_device(device, lambda: _check(load_library().hkv_gather_quant(
-        ctypes.byref(quant), pk, pv, NP, s, Kp, P_tok, H, d, r, at, step, kc, vc, kb, w, wn, _stream(stream)), where))
+    _launch(where, device, stream, load_library().hkv_gather_quant, ctypes.byref(quant), pk, pv, NP, s, Kp, P_tok, H, d, r, at,
+            step, kc, vc, kb, w, wn)
 
 
 def hkv_attn_quant_workspace_size(T: int, Hq: int, H: int, d: int, Kp: int, P_tok: int) -> int:
@@ -643,9 +650,8 @@ def hkv_attn_quant(quant: Quant, Q, page_k_ptrs, page_v_ptrs, sel, Kp, P_tok, H,
     o = _tensor(out, "out", where, device, out.dtype, Q.shape)
     ls = None if lse is None else _tensor(lse, "lse", where, device, torch.float32, (T, Hq))
     n = None if n_rows is None else _tensor(n_rows.view(-1), "n_rows", where, device, torch.int32, (1,))
-    _on_device(device, lambda: _check(load_library().hkv_attn_quant(
-        ctypes.byref(quant), q, T, Hq, pk, pv, NP, s, Kp, P_tok, H, d, n, scale, o, 1 if out.dtype == torch.bfloat16 else 0, ls,
-        w, wn, _stream(stream)), where))
+    _launch(where, device, stream, load_library().hkv_attn_quant, ctypes.byref(quant), q, T, Hq, pk, pv, NP, s, Kp, P_tok, H, d,
+            n, scale, o, 1 if out.dtype == torch.bfloat16 else 0, ls, w, wn)
 
 
 # ---------------------------------------------------------------- tracing

@@ -933,6 +933,12 @@ hsa_status_t hsa_forward_reuse(const hsa_config_t* cfg, const hsa_bf16* Q, const
 
 // ------------------------------------------------------------------ rotary positions
 
+// The rotary and quantised-page kernels index a row's columns in 32 bits.
+constexpr int kMostHeads = 16384;
+static hsa_status_t check_many_heads(const char* fn, int H) {
+  return H <= kMostHeads ? HSA_OK : fail(HSA_ERR_UNSUPPORTED, "%s: H = %d heads (supported: up to %d)", fn, H, kMostHeads);
+}
+
 static int dtype_bytes(int dtype) {
   return dtype == HSA_DTYPE_FP32 ? 4 : (dtype == HSA_DTYPE_BF16 || dtype == HSA_DTYPE_FP16) ? 2 : 0;
 }
@@ -983,6 +989,7 @@ static hsa_status_t rows_args(const char* fn, const char* what, const hsa_rows_t
   if (!x || (!x->data && T > 0)) return fail(HSA_ERR_INVALID_ARG, "%s: %s is NULL", fn, what);
   if (!aligned16(x->data)) return fail(HSA_ERR_INVALID_ARG, "%s: %s is not 16-byte aligned", fn, what);
   TRY(check_heads(fn, x->H, d));
+  TRY(check_many_heads(fn, x->H));
   const long long unit = 16 / dtype_bytes(dtype);
   if (x->token_stride % unit != 0 || x->head_stride % unit != 0)
     return fail(HSA_ERR_INVALID_ARG, "%s: %s: strides %lld, %lld are not multiples of 16 bytes", fn, what, x->token_stride,
@@ -1069,6 +1076,7 @@ static hsa_status_t quant_args(const char* fn, const hkv_quant_t* q, int P_tok, 
   if (t_fault == HSA_FAULT_ARG) return fail(HSA_ERR_INVALID_ARG, "%s: injected argument failure", fn);
   if (!q) return fail(HSA_ERR_INVALID_ARG, "%s: quant is NULL", fn);
   TRY(check_heads(fn, H, d));
+  TRY(check_many_heads(fn, H));
   if (P_tok < 1) return fail(HSA_ERR_INVALID_ARG, "%s: P_tok = %d must be >= 1", fn, P_tok);
   if (q->format < HKV_QUANT_E4M3 || q->format > HKV_QUANT_INT4)
     return fail(HSA_ERR_INVALID_ARG, "%s: quant format = %d", fn, q->format);
@@ -1153,11 +1161,13 @@ static hsa_status_t attn_quant_layout(const char* fn, int T, int Hq, int H, int 
   TRY(check_heads(fn, H, d));
   if (T < 0) return fail(HSA_ERR_INVALID_ARG, "%s: T = %d must be >= 0", fn, T);
   if (T > 64) return fail(HSA_ERR_UNSUPPORTED, "%s: T = %d queries (supported: up to 64; assemble the cache for more)", fn, T);
+  TRY(check_many_heads(fn, H));
+  TRY(check_many_heads(fn, Hq));
   if (Hq < 1 || Hq % H != 0) return fail(HSA_ERR_INVALID_ARG, "%s: Hq = %d is not a multiple of H = %d", fn, Hq, H);
   if (Kp < 1 || P_tok < 1) return fail(HSA_ERR_INVALID_ARG, "%s: Kp = %d, P_tok = %d must be >= 1", fn, Kp, P_tok);
   if ((long long)Kp * P_tok > 0x7fffffffLL)
     return fail(HSA_ERR_UNSUPPORTED, "%s: Kp * P_tok = %lld rows exceed 2^31 - 1", fn, (long long)Kp * P_tok);
-  *splits = T > 0 ? hsa::attn_quant_splits(T, Hq, H, d, Kp, P_tok) : 1;
+  *splits = T > 0 ? hsa::attn_quant_most_splits(T, Hq, H, Kp, P_tok) : 1;
   const size_t rows = *splits > 1 ? (size_t)*splits * T * Hq : 0;
   *part_ml = 256 + align256(rows * d * sizeof(float));
   *total = *part_ml + align256(rows * sizeof(float2));

@@ -22,10 +22,20 @@
 //        are taken relative to a running power of two per group (`vref`), which only rises;
 //        the accumulators are rescaled when it does, as when the running maximum rises.
 //
-// Work: a warp takes 16-key tiles of one page and head; a CTA is 4 warps on one
-// (split of the rows, head, query tile); the splits are joined by a second kernel in order
-// (deterministic).  A tile never straddles pages; keys behind a page's or the cache's end
-// are read from the tile's last valid row and get no weight.
+// Work: a CTA takes tiles of a split of the rows, four warps with 32 keys of a head each: of
+// four neighbouring heads where there are so many, so that a row's codes are fetched in runs of
+// 256 to 512 bytes and its scales in 16-byte vectors (with a head to a CTA the scales, 4 bytes
+// from each 32-byte sector, were half of all requests: 124 us instead of 96 for one token over
+// 49920 rows of 40 heads).  Tiles are on their way to a ring in shared memory while one is
+// worked on; small CTAs, three to an SM, drift apart and keep the loads going where one of 8 or
+// 12 warps stops at its barrier (199680 rows: 329 us, 0.98 of the copy rate, against 395 to
+// 425).  The splits are joined by a second kernel in order (deterministic).  A tile never
+// straddles pages; what lies behind a page's or the cache's end is fetched as zeros and gets no
+// weight.
+//
+// Short caches are bound by their latency: two launches, the way from the row count to the page
+// table to the rows, and the join cost 9 us together.  4-bit codes are bound by the instructions
+// that turn them into operands (49920 rows of 12 heads: 36 us against 37 us in 8 bits).
 #include "common.cuh"
 #include "kernels.h"
 #include "quant.cuh"
@@ -35,13 +45,17 @@ namespace {
 
 constexpr int kAqWarps = 4;
 constexpr int kAqThreads = kAqWarps * 32;
-#ifndef AQ_S
-#define AQ_S 3
-#define AQ_C 3
-#endif
-constexpr int kAqStages = AQ_S;  // tiles of a warp's ring
-constexpr int kAqCtas = AQ_C;    // on an SM
-constexpr int kAqCtasWide = 2;   // ... with 16 queries to a tile
+constexpr int kAqRows = 32;    // keys of a warp's unit
+constexpr int kAqStages = 2;   // tiles of the ring
+constexpr int kAqMostCtas = 4;
+
+// CTAs on an SM, with up to 8 (NT = 1) or 16 queries to a tile: as many as registers and the ring allow.
+template <int FMT, int D, int GROUP, int NT>
+constexpr int ctas_per_sm() {
+  if (NT == 2) return 2;
+  if (D == 64) return 4;
+  return code_bits<FMT>() == 8 && GROUP == 32 ? 2 : 3;
+}
 
 __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -64,6 +78,17 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 __device__ __forceinline__ uint32_t hsub2_u(uint32_t a, uint32_t b) {
   const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&d);
+}
+
+// The low two nibbles of each half of w as halves: p0 the lowest of both, p1 the next.  Flipping
+// a nibble's sign bit gives n + 8, which becomes the low bits of 1024 + (n + 8), or, left where
+// it is, of 1024 + 16 (n + 8).
+__device__ __forceinline__ void nibbles(uint32_t w, uint32_t& p0, uint32_t& p1) {
+  p0 = hsub2_u((w & 0x000f000fu) ^ 0x64086408u, 0x64086408u);  // - 1032
+  const uint32_t x = (w & 0x00f000f0u) ^ 0x64806480u, sixteenth = 0x2c002c00u, minus72 = 0xd480d480u;
+  const __half2 y = __hfma2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&sixteenth),
+                            *reinterpret_cast<const __half2*>(&minus72));
+  p1 = *reinterpret_cast<const uint32_t*>(&y);
 }
 
 // N bytes of codes a thread reads at once, as words (N = 2: the low half of one).
@@ -92,21 +117,31 @@ __device__ __forceinline__ Raw<N> read_raw(const char* p) {
   return r;
 }
 
+// Neighbouring heads of a CTA: their codes and scales of a row are fetched in one piece.
+inline int attn_quant_heads(int H) { return H % 4 == 0 ? 4 : H % 2 == 0 ? 2 : 1; }
+
+// Splits of the rows: one wave of CTAs, at least a tile to each.
+inline int attn_quant_splits_of(int ctas_per_sm, int T, int Hq, int H, int Kp, int P_tok) {
+  const int cols = T * (Hq / H), heads = attn_quant_heads(H), tile = kAqRows * kAqWarps / heads;
+  const long long tiles = (long long)Kp * ((P_tok + tile - 1) / tile);
+  const long long units = (long long)(H / heads) * (cols <= 8 ? 1 : (cols + 15) / 16);
+  long long n = 148LL * ctas_per_sm / units;
+  if (n > tiles) n = tiles;
+  return (int)(n < 1 ? 1 : n);
+}
+
 // Four codes of a thread's run starting at code 4 s (for 4 bits: codes 0, 4, 1, 5 of its
 // eight when s is even, 2, 6, 3, 7 when odd) as two operand registers.
 template <int FMT>
 __device__ __forceinline__ void four_codes(const uint32_t* w, int s, uint32_t& p0, uint32_t& p1) {
   if constexpr (FMT == HKV_QUANT_E4M3) {
-    p0 = e4m3x2_to_half2(w[s]);
-    p1 = e4m3x2_to_half2(w[s] >> 16);
+    e4m3x4_to_half2(w[s], p0, p1);
   } else if constexpr (FMT == HKV_QUANT_INT8) {
     const uint32_t u = w[s] ^ 0x80808080u;
     p0 = hsub2_u(__byte_perm(u, 0x64646464u, 0x4140), 0x64806480u);  // 1024 + u - 1152
     p1 = hsub2_u(__byte_perm(u, 0x64646464u, 0x4342), 0x64806480u);
   } else {
-    const uint32_t u = (w[s >> 1] ^ 0x88888888u) >> (s & 1 ? 8 : 0);
-    p0 = hsub2_u((u & 0x000f000fu) | 0x64006400u, 0x64086408u);  // 1024 + u - 1032
-    p1 = hsub2_u(((u >> 4) & 0x000f000fu) | 0x64006400u, 0x64086408u);
+    nibbles(w[s >> 1] >> (s & 1 ? 8 : 0), p0, p1);
   }
 }
 // Where code i (0..3) of step s sits in the thread's run of codes.
@@ -120,15 +155,11 @@ __device__ __forceinline__ constexpr int code_at(int s, int i) {
 template <int FMT>
 __device__ __forceinline__ void two_keys(const uint32_t* a, const uint32_t* b, int m, uint32_t& p0, uint32_t& p1) {
   if constexpr (FMT == HKV_QUANT_INT4) {
-    const uint32_t u = __byte_perm(a[m >> 2], b[m >> 2], m & 2 ? 0x7632 : 0x5410) ^ 0x88888888u;
-    const int sh = m & 1 ? 8 : 0;
-    p0 = hsub2_u(((u >> sh) & 0x000f000fu) | 0x64006400u, 0x64086408u);
-    p1 = hsub2_u(((u >> (sh + 4)) & 0x000f000fu) | 0x64006400u, 0x64086408u);
+    nibbles(__byte_perm(a[m >> 1 >> 1], b[m >> 1 >> 1], m & 2 ? 0x7632 : 0x5410) >> (m & 1 ? 8 : 0), p0, p1);
   } else {
     const uint32_t u = __byte_perm(a[m >> 1], b[m >> 1], m & 1 ? 0x7362 : 0x5140);  // a0 b0 a1 b1
     if constexpr (FMT == HKV_QUANT_E4M3) {
-      p0 = e4m3x2_to_half2(u);
-      p1 = e4m3x2_to_half2(u >> 16);
+      e4m3x4_to_half2(u, p0, p1);
     } else {
       const uint32_t x = u ^ 0x80808080u;
       p0 = hsub2_u(__byte_perm(x, 0x64646464u, 0x4140), 0x64806480u);
@@ -143,17 +174,30 @@ __device__ __forceinline__ float pow2_below(float x) {  // the power of two at o
 }
 __device__ __forceinline__ float pow2_inverse(float p) { return __uint_as_float((254u << 23) - __float_as_uint(p)); }
 
-// A warp's ring of 16-key tiles in shared memory: codes of K and of V, rows padded by 16 bytes
-// (the operand reads below are then free of bank conflicts at 128-byte rows), and scales.
+// The CTA's ring of tiles in shared memory.  A tile is some rows of a few neighbouring heads,
+// cut into a unit of kAqRows rows of one head for each warp: codes of K and of V, rows padded
+// by 16 bytes (the operand reads below are then free of bank conflicts at 128-byte rows), and
+// behind the units the rows' scales, as they lie in the page.
 template <int FMT, int D, int GROUP>
 struct Stage {
   static constexpr int kRow = D * code_bits<FMT>() / 8, kPitch = kRow + 16;
-  static constexpr int kScales = 16 * (D / GROUP) * 4;  // bytes of a tile's
-  static constexpr int kV = 16 * kPitch, kKs = 2 * kV, kVs = kKs + kScales, kBytes = kVs + kScales;
+  static constexpr int kV = kAqRows * kPitch, kUnit = 2 * kV;
+  static constexpr int kScales = kAqWarps * kAqRows * (D / GROUP) * 4;  // bytes of K's, or V's, scales of a tile
+  static constexpr int kKs = kAqWarps * kUnit, kVs = kKs + kScales, kBytes = kVs + kScales;
 };
 
-template <int FMT, int D, int GROUP, int NT>
-__global__ void __launch_bounds__(kAqThreads, NT == 1 ? kAqCtas : kAqCtasWide) attn_quant_kernel(const AttnQuantArgs a) {
+// Column d of a row: v / sum, the weights taken relative to 2^top (-inf: to 1).
+__device__ __forceinline__ void write_out(const AttnQuantArgs& a, long long row, int D, int d, float v, float top,
+                                          float sum) {
+  const float r = sum == 0.f ? 0.f : v / sum;
+  if (a.out_f32) a.out_f32[row * D + d] = r;
+  else a.out_bf16[row * D + d] = (uint16_t)pack_bf16x2(r, 0.f);
+  if (d == 0 && a.lse)
+    a.lse[row] = sum == 0.f ? -INFINITY : (top == -INFINITY ? 0.f : top) * 0.69314718055994531f + logf(sum);
+}
+
+template <int FMT, int D, int GROUP, int NT, int HEADS>
+__global__ void __launch_bounds__(kAqThreads, (ctas_per_sm<FMT, D, GROUP, NT>())) attn_quant_kernel(const AttnQuantArgs a) {
   constexpr int G = D / GROUP;               // groups of a head
   constexpr int KS = GROUP / 16;             // product steps of a group (S), and 16-column tiles of a group (O)
   constexpr int BITS = code_bits<FMT>();
@@ -161,41 +205,48 @@ __global__ void __launch_bounds__(kAqThreads, NT == 1 ? kAqCtas : kAqCtasWide) a
   constexpr int VB = GROUP / 8 * BITS / 8;   // ... of a value row
   constexpr int COLS = 8 * NT;               // queries of a tile
   using St = Stage<FMT, D, GROUP>;
-  extern __shared__ __align__(16) char ring_all[];
+  constexpr int M = kAqRows / 16;              // 16-key products of a unit
+  extern __shared__ __align__(16) char ring[];
   __shared__ float s_m[kAqWarps][COLS], s_l[kAqWarps][COLS];
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int g = lane / 4, t = lane % 4;
-  const int h = blockIdx.x % a.q.H, split = blockIdx.x / a.q.H;
-  const int share = a.Hq / a.q.H;            // query heads of this key head
+  // the CTA's warps: HEADS neighbouring heads, kAqWarps / HEADS units of rows of each
+  const int split = blockIdx.x / (a.q.H / HEADS), h0 = (blockIdx.x - split * (a.q.H / HEADS)) * HEADS;
+  const int own_head = warp % HEADS, own_rows = warp / HEADS * kAqRows, h = h0 + own_head;
+  const int share = a.Hq / a.q.H;            // query heads of a key head
   const int cols = a.T * share, col0 = blockIdx.y * COLS;
   const int P = a.q.P_tok;
 
   // Tiles of the first n rows: tiles_page of each whole page, then those of the last one.
+  constexpr int TILE = kAqRows * kAqWarps / HEADS;
   const long long all = (long long)a.Kp * P;
   long long n_rows = a.n_rows ? (long long)*a.n_rows : all;
   n_rows = n_rows < 0 ? 0 : (n_rows > all ? all : n_rows);
-  const int tiles_page = (P + 15) / 16;
+  const int tiles_page = (P + TILE - 1) / TILE;
   const int whole = (int)(n_rows / P), rest = (int)(n_rows - (long long)whole * P);
-  const int tiles = whole * tiles_page + (rest + 15) / 16;
+  const int tiles = whole * tiles_page + (rest + TILE - 1) / TILE;
   const int per = (tiles + a.splits - 1) / a.splits;
-  const int tile_end = (int)min((long long)tiles, (long long)(split + 1) * per);
+  const int first = (int)min((long long)tiles, (long long)split * per), rounds = min(per, tiles - first);
 
-  // asking for tiles: this warp's are warp, warp + kAqWarps, ... of the split's
-  char* ring = ring_all + warp * kAqStages * St::kBytes;
+  // asking for tiles: a row's codes are HEADS * kRow bytes next to each other, its scales
+  // HEADS * G floats
   const uint32_t ring_s = smem_u32(ring);
-  constexpr int CH = St::kRow / 16;          // 16-byte vectors of a row
-  constexpr int PER = 16 * CH / 32;          // ... of a tile that a lane copies
-  const int my_row = lane / CH, my_vec = lane % CH;
-  const long long row_step = (long long)a.q.H * St::kRow;
-  long long tile_l = (long long)split * per + warp;
-  int tile = tile_l < tile_end ? (int)tile_l : tile_end;
-  int slot = tile / tiles_page, in_page = tile - slot * tiles_page, known = -1;
+  constexpr int CH = HEADS * St::kRow / 16;          // 16-byte vectors of a row
+  constexpr int ROWS_AT_ONCE = kAqThreads / CH;      // rows that the CTA copies at once
+  constexpr int PER = TILE / ROWS_AT_ONCE;
+  const int my_row = tid / CH, my_vec = tid % CH;
+  const int my_head = my_vec / (CH / HEADS), my_col = my_vec % (CH / HEADS) * 16;
+  constexpr int SF = HEADS * G;                      // scales of a row
+  const long long row_step = (long long)a.q.H * St::kRow, scale_step = (long long)a.q.H * 4 * G;
+  const bool wide = SF % 4 == 0 && scale_step % 16 == 0;  // scales in 16-byte vectors (else one by one)
+  const int piece = wide ? 4 : 1, pieces = SF / piece;
+  int asked_tile = 0, slot = first / tiles_page, in_page = first - slot * tiles_page, known = -1;
   const char *kbase = nullptr, *vbase = nullptr;
-  unsigned long long valid_of = 0;  // rows of the tiles asked for, a byte each, the next to be worked on first
+  unsigned long long valid_of = 0;  // rows of the tiles asked for, 16 bits each, the next to be worked on first
   int asked = 0;
   auto ask = [&](int stage) {
     int valid = 0;
-    if (tile < tile_end) {
+    if (asked_tile < rounds) {
       if (slot != known) {
         known = slot;
         const int p = a.sel[slot];
@@ -208,30 +259,46 @@ __global__ void __launch_bounds__(kAqThreads, NT == 1 ? kAqCtas : kAqCtasWide) a
         }
       }
       if (kbase) {
-        const int row0 = in_page * 16;
-        valid = min((slot < whole ? P : rest) - row0, 16);
+        const int row0 = in_page * TILE;
+        valid = min((slot < whole ? P : rest) - row0, TILE);
         const uint32_t dst = ring_s + stage * St::kBytes;
-        const long long from = ((long long)row0 * a.q.H + h) * St::kRow + my_vec * 16;
+        const long long from = (row0 + my_row) * row_step + h0 * St::kRow + my_vec * 16;
+        const char *k = kbase + from, *v = vbase + from;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-          const int row = my_row + i * (32 / CH);
-          const long long src = from + (row < valid ? row * row_step : 0);
-          cp_async_zero<16>(dst + row * St::kPitch + my_vec * 16, kbase + src, row < valid);
-          cp_async_zero<16>(dst + St::kV + row * St::kPitch + my_vec * 16, vbase + src, row < valid);
+          const int row = my_row + i * ROWS_AT_ONCE;
+          const uint32_t to = dst + (row / kAqRows * HEADS + my_head) * St::kUnit + row % kAqRows * St::kPitch + my_col;
+          const bool on = row < valid;  // zeros behind the last row
+          cp_async_zero<16>(to, on ? k : kbase, on);
+          cp_async_zero<16>(to + St::kV, on ? v : vbase, on);
+          k += ROWS_AT_ONCE * row_step;
+          v += ROWS_AT_ONCE * row_step;
         }
-        const int row = lane & 15;
-        const long long head_row = (long long)(row0 + (row < valid ? row : 0)) * a.q.H + h;
-        cp_async_zero<4 * G>(dst + (lane < 16 ? St::kKs : St::kVs) + row * 4 * G,
-                             (lane < 16 ? kbase : vbase) + a.q.scale_offset + head_row * 4 * G, row < valid);
+        for (int i = tid; i < TILE * pieces; i += kAqThreads) {
+          const int row = i / pieces, at = i - row * pieces;
+          const bool on = row < valid;
+          const long long src = a.q.scale_offset + (on ? (row0 + row) * scale_step + h0 * 4 * G + at * piece * 4 : 0);
+          const uint32_t to = dst + St::kKs + (row * SF + at * piece) * 4;
+          if (wide) {
+            cp_async_zero<16>(to, kbase + src, on);
+            cp_async_zero<16>(to + St::kScales, vbase + src, on);
+          } else {
+            cp_async_zero<4>(to, kbase + src, on);
+            cp_async_zero<4>(to + St::kScales, vbase + src, on);
+          }
+        }
       }
-      tile += kAqWarps;
-      for (in_page += kAqWarps; in_page >= tiles_page; in_page -= tiles_page) ++slot;
+      ++asked_tile;
+      if (++in_page == tiles_page) {
+        in_page = 0;
+        ++slot;
+      }
     }
     cp_async_commit();
-    valid_of |= (unsigned long long)valid << (8 * asked);
+    valid_of |= (unsigned long long)valid << (16 * asked);
     ++asked;
   };
-  const int rounds = tile < tile_end ? (tile_end - tile + kAqWarps - 1) / kAqWarps : 0;
+  static_assert(kAqStages <= 4 && TILE % ROWS_AT_ONCE == 0 && kAqWarps % HEADS == 0, "four tiles asked for at most");
 #pragma unroll
   for (int s = 0; s < kAqStages - 1; ++s) ask(s);
 
@@ -267,13 +334,15 @@ __global__ void __launch_bounds__(kAqThreads, NT == 1 ? kAqCtas : kAqCtasWide) a
   }
 
   float o[NT][G * KS][4];
-  float m[NT][2], l[NT][2];
-  float vref[G];
+  // the reference that scores are taken relative to, and the value scales of each group: raised
+  // when something in a tile is more than 2^6 above them, so that weights stay below 2^12
+  float m[NT][2], ref[NT][2], l[NT][2], vref[G];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
 #pragma unroll
     for (int k = 0; k < G * KS; ++k) o[n][k][0] = o[n][k][1] = o[n][k][2] = o[n][k][3] = 0.f;
     m[n][0] = m[n][1] = -INFINITY;
+    ref[n][0] = ref[n][1] = 0.f;  // m, or 0 while that is -inf
     l[n][0] = l[n][1] = 0.f;
   }
 #pragma unroll
@@ -281,92 +350,91 @@ __global__ void __launch_bounds__(kAqThreads, NT == 1 ? kAqCtas : kAqCtasWide) a
 
   for (int i = 0, stage = 0; i < rounds; ++i, stage = stage == kAqStages - 1 ? 0 : stage + 1) {
     cp_async_wait<kAqStages - 2>();
-    __syncwarp();  // all lanes' copies are there, and all are done with the stage before
-    const int valid = (int)(valid_of & 255u);
-    valid_of >>= 8;
+    __syncthreads();  // all copies are there, and all warps are done with the stage before
+    const int valid = (int)(valid_of & 0xffffu) - own_rows;
+    valid_of >>= 16;
     --asked;
     ask(stage == 0 ? kAqStages - 1 : stage - 1);
-    if (valid == 0) continue;
-    // keys g and g + 8; values 2t, 2t + 1, 2t + 8, 2t + 9
-    const char* st = ring + stage * St::kBytes;
-    Raw<KB> kw[2][G];
-    Raw<VB> vw[4][G];
-    float ks[2][G], vs[2][G];  // scales of rows g and g + 8
+    if (valid <= 0) continue;
+    const char* st = ring + stage * St::kBytes + warp * St::kUnit;
+    const float* k_scale = reinterpret_cast<const float*>(ring + stage * St::kBytes + St::kKs) + own_rows * SF + own_head * G;
+    const float* v_scale = k_scale + St::kScales / 4;
+    // S = K q, keys g and g + 8 of each 16
+    float s[M][NT][4];
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
+    for (int mi = 0; mi < M; ++mi) {
 #pragma unroll
       for (int k = 0; k < G; ++k) {
-        kw[r][k] = read_raw<KB>(st + (g + 8 * r) * St::kPitch + k * GROUP * BITS / 8 + t * KB);
-        ks[r][k] = *reinterpret_cast<const float*>(st + St::kKs + ((g + 8 * r) * G + k) * 4);
-        vs[r][k] = *reinterpret_cast<const float*>(st + St::kVs + ((g + 8 * r) * G + k) * 4);
-      }
+        const char* row = st + (16 * mi + g) * St::kPitch + k * GROUP * BITS / 8 + t * KB;
+        const Raw<KB> k0 = read_raw<KB>(row), k1 = read_raw<KB>(row + 8 * St::kPitch);
+        const float ks0 = k_scale[(16 * mi + g) * SF + k], ks1 = k_scale[(16 * mi + g + 8) * SF + k];
+        float part[NT][4];
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
+        for (int n = 0; n < NT; ++n) part[n][0] = part[n][1] = part[n][2] = part[n][3] = 0.f;
 #pragma unroll
-      for (int k = 0; k < G; ++k)
-        vw[r][k] = read_raw<VB>(st + St::kV + (2 * t + (r & 1) + 4 * (r & 2)) * St::kPitch + k * GROUP * BITS / 8 + g * VB);
-    // S = K q
-    float s[NT][4];
+        for (int q = 0; q < KS; ++q) {
+          uint32_t f[4];
+          four_codes<FMT>(k0.w, q, f[0], f[2]);
+          four_codes<FMT>(k1.w, q, f[1], f[3]);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+          for (int n = 0; n < NT; ++n) mma16816(part[n], f, qf[n][k * KS + q][0], qf[n][k * KS + q][1]);
+        }
 #pragma unroll
-    for (int k = 0; k < G; ++k) {
-      float part[NT][4];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) part[n][0] = part[n][1] = part[n][2] = part[n][3] = 0.f;
-#pragma unroll
-      for (int st = 0; st < KS; ++st) {
-        uint32_t f[4];
-        four_codes<FMT>(kw[0][k].w, st, f[0], f[2]);
-        four_codes<FMT>(kw[1][k].w, st, f[1], f[3]);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) mma16816(part[n], f, qf[n][k * KS + st][0], qf[n][k * KS + st][1]);
-      }
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        s[n][0] = fmaf(part[n][0], ks[0][k], s[n][0]);
-        s[n][1] = fmaf(part[n][1], ks[0][k], s[n][1]);
-        s[n][2] = fmaf(part[n][2], ks[1][k], s[n][2]);
-        s[n][3] = fmaf(part[n][3], ks[1][k], s[n][3]);
+        for (int n = 0; n < NT; ++n) {
+          s[mi][n][0] = k == 0 ? part[n][0] * ks0 : fmaf(part[n][0], ks0, s[mi][n][0]);
+          s[mi][n][1] = k == 0 ? part[n][1] * ks0 : fmaf(part[n][1], ks0, s[mi][n][1]);
+          s[mi][n][2] = k == 0 ? part[n][2] * ks1 : fmaf(part[n][2], ks1, s[mi][n][2]);
+          s[mi][n][3] = k == 0 ? part[n][3] * ks1 : fmaf(part[n][3], ks1, s[mi][n][3]);
+        }
       }
     }
-    // softmax weights of this tile; p of rows g and g + 8, columns 2t and 2t + 1
-    const bool in0 = g < valid, in1 = g + 8 < valid;
-    float alpha[NT][2];
-    bool moved = false;
+    // value scales of keys g and g + 8, and whether a reference has to be raised
+    float vs[M][2][G];
+    bool high = false;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
+    for (int mi = 0; mi < M; ++mi) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float x = in0 ? s[n][e] * qs[n][e] : -INFINITY;
-        float y = in1 ? s[n][2 + e] * qs[n][e] : -INFINITY;
-        float top = fmaxf(x, y);
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float x = s[mi][n][e] * qs[n][e & 1];
+          s[mi][n][e] = 16 * mi + g + 8 * (e >> 1) < valid ? x : -INFINITY;
+          high |= s[mi][n][e] > m[n][e & 1] + 6.f;
+        }
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int k = 0; k < G; ++k) {
+          vs[mi][r][k] = v_scale[(16 * mi + g + 8 * r) * SF + k];
+          high |= fabsf(vs[mi][r][k]) > 64.f * vref[k];
+        }
+    }
+    if (__any_sync(0xffffffffu, high)) {
+      float alpha[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float top = m[n][e];
+#pragma unroll
+          for (int mi = 0; mi < M; ++mi) top = fmaxf(top, fmaxf(s[mi][n][e], s[mi][n][2 + e]));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+          ref[n][e] = top == -INFINITY ? 0.f : top;
+          alpha[n][e] = exp2f(m[n][e] - ref[n][e]);
+          m[n][e] = top;
+          l[n][e] *= alpha[n][e];
+        }
+#pragma unroll
+      for (int k = 0; k < G; ++k) {
+        float top = 0.f;
+#pragma unroll
+        for (int mi = 0; mi < M; ++mi) top = fmaxf(top, fmaxf(fabsf(vs[mi][0][k]), fabsf(vs[mi][1][k])));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-        const float next = fmaxf(m[n][e], top);
-        const float ref = next == -INFINITY ? 0.f : next;
-        alpha[n][e] = exp2f(m[n][e] - ref);
-        moved |= next != m[n][e];
-        m[n][e] = next;
-        x = exp2f(x - ref);
-        y = exp2f(y - ref);
-        l[n][e] = l[n][e] * alpha[n][e] + (x + y);
-        s[n][e] = x;
-        s[n][2 + e] = y;
-      }
-    }
-    // O += V w, group by group
-    const bool rescale = __any_sync(0xffffffffu, moved);
-#pragma unroll
-    for (int k = 0; k < G; ++k) {
-      const float v0 = in0 ? vs[0][k] : 0.f, v1 = in1 ? vs[1][k] : 0.f;
-      float top = fmaxf(fabsf(v0), fabsf(v1));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-      const float next = fmaxf(vref[k], pow2_below(top));
-      if (rescale || next != vref[k]) {
+        const float next = fmaxf(vref[k], pow2_below(top));
         const float beta = vref[k] * pow2_inverse(next);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -376,36 +444,54 @@ __global__ void __launch_bounds__(kAqThreads, NT == 1 ? kAqCtas : kAqCtasWide) a
             for (int e = 0; e < 4; ++e) o[n][k * KS + mt][e] *= alpha[n][e & 1] * beta;
         vref[k] = next;
       }
-      const float inv = pow2_inverse(next);
-      const float r0 = v0 * inv, r1 = v1 * inv;
-      uint32_t hi[NT][2], lo[NT][2];
+    }
+#pragma unroll
+    for (int mi = 0; mi < M; ++mi) {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float w0 = s[n][2 * i] * (i ? r1 : r0), w1 = s[n][2 * i + 1] * (i ? r1 : r0);
-          const uint32_t hh = pack_half2(w0, w1);
-          const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hh));
-          hi[n][i] = movmatrix(hh);
-          lo[n][i] = movmatrix(pack_half2(w0 - back.x, w1 - back.y));
+        for (int e = 0; e < 4; ++e) {
+          s[mi][n][e] = exp2f(s[mi][n][e] - ref[n][e & 1]);
+          l[n][e & 1] += s[mi][n][e];
         }
+      // O += V w, group by group; values 2t, 2t + 1, 2t + 8, 2t + 9
 #pragma unroll
-      for (int mt = 0; mt < KS; ++mt) {
-        uint32_t f[4];
-        two_keys<FMT>(vw[0][k].w, vw[1][k].w, mt, f[0], f[1]);
-        two_keys<FMT>(vw[2][k].w, vw[3][k].w, mt, f[2], f[3]);
+      for (int k = 0; k < G; ++k) {
+        Raw<VB> vw[4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          mma16816(o[n][k * KS + mt], f, hi[n][0], hi[n][1]);
-          mma16816(o[n][k * KS + mt], f, lo[n][0], lo[n][1]);
+        for (int r = 0; r < 4; ++r)
+          vw[r] = read_raw<VB>(st + St::kV + (16 * mi + 2 * t + (r & 1) + 4 * (r & 2)) * St::kPitch +
+                               k * GROUP * BITS / 8 + g * VB);
+        const float inv = pow2_inverse(vref[k]);
+        uint32_t hi[NT][2], lo[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float scale = vs[mi][r][k] * inv;
+            const float w0 = s[mi][n][2 * r] * scale, w1 = s[mi][n][2 * r + 1] * scale;
+            const uint32_t hh = pack_half2(w0, w1);
+            const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hh));
+            hi[n][r] = movmatrix(hh);
+            lo[n][r] = movmatrix(pack_half2(w0 - back.x, w1 - back.y));
+          }
+#pragma unroll
+        for (int mt = 0; mt < KS; ++mt) {
+          uint32_t f[4];
+          two_keys<FMT>(vw[0].w, vw[1].w, mt, f[0], f[1]);
+          two_keys<FMT>(vw[2].w, vw[3].w, mt, f[2], f[3]);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma16816(o[n][k * KS + mt], f, hi[n][0], hi[n][1]);
+            mma16816(o[n][k * KS + mt], f, lo[n][0], lo[n][1]);
+          }
         }
       }
     }
   }
 
+  // Join the warps, in order.  The ring is free once all of them are done with it.
   cp_async_wait<0>();
-  float(*s_o)[D] = reinterpret_cast<float(*)[D]>(ring_all);  // after the barrier below the ring is free
-  // Join the warps in order.
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -420,123 +506,178 @@ __global__ void __launch_bounds__(kAqThreads, NT == 1 ? kAqCtas : kAqCtasWide) a
       }
     }
   __syncthreads();
-  float share_of[NT][2];  // 2^(this warp's maximum - the CTA's)
+  float* s_o = reinterpret_cast<float*>(ring);  // [warp][column][kOPitch]
+  constexpr int kOPitch = D + 4;
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       float top = -INFINITY;
-      for (int w = 0; w < kAqWarps; ++w) top = fmaxf(top, s_m[w][n * 8 + 2 * t + e]);
-      share_of[n][e] = top == -INFINITY ? 0.f : exp2f(m[n][e] - top);
+#pragma unroll
+      for (int w = 0; w < kAqWarps; w += HEADS) top = fmaxf(top, s_m[w + own_head][n * 8 + 2 * t + e]);
+      const float part = top == -INFINITY ? 0.f : exp2f(m[n][e] - top);  // a warp without rows has m = -inf and o = 0
+      float* dst = s_o + (warp * COLS + n * 8 + 2 * t + e) * kOPitch;
+#pragma unroll
+      for (int k = 0; k < G * KS; ++k) {
+        const int d = (k / KS) * GROUP + g * (GROUP / 8) + 2 * (k % KS);
+        const float f = vref[k / KS];
+        *reinterpret_cast<float2*>(dst + d) = make_float2(o[n][k][e] * f * part, o[n][k][2 + e] * f * part);
+      }
     }
-  for (int w = 0; w < kAqWarps; ++w) {
-    if (warp == w) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int k = 0; k < G * KS; ++k)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int d = (k / KS) * GROUP + g * (GROUP / 8) + 2 * (k % KS) + (e >> 1);
-            float& dst = s_o[n * 8 + 2 * t + (e & 1)][d];
-            // a warp without rows has nothing to add (its maximum is -inf)
-            const float add = o[n][k][e] * vref[k / KS] * share_of[n][e & 1];
-            dst = w == 0 ? add : dst + add;
-          }
-    }
-    __syncthreads();
-  }
-  for (int i = threadIdx.x; i < COLS * D; i += kAqThreads) {
-    const int c = i / D, d = i % D, col = col0 + c;
-    if (col >= cols) break;
+  __syncthreads();
+  for (int i = tid; i < HEADS * COLS * D; i += kAqThreads) {
+    const int hw = i / (COLS * D), c = i / D % COLS, d = i % D, col = col0 + c;
+    if (col >= cols) continue;
     float top = -INFINITY;
-    for (int w = 0; w < kAqWarps; ++w) top = fmaxf(top, s_m[w][c]);
-    float sum = 0.f;
-    for (int w = 0; w < kAqWarps; ++w) sum += top == -INFINITY ? s_l[w][c] : s_l[w][c] * exp2f(s_m[w][c] - top);
-    const float v = s_o[c][d];
-    const long long row = (long long)(col / share) * a.Hq + h * share + col % share;
+#pragma unroll
+    for (int w = 0; w < kAqWarps; w += HEADS) top = fmaxf(top, s_m[w + hw][c]);
+    float sum = 0.f, v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kAqWarps; w += HEADS) {
+      sum += top == -INFINITY ? s_l[w + hw][c] : s_l[w + hw][c] * exp2f(s_m[w + hw][c] - top);
+      v += s_o[((w + hw) * COLS + c) * kOPitch + d];
+    }
+    const long long row = (long long)(col / share) * a.Hq + (h0 + hw) * share + col % share;
     if (a.splits > 1) {
-      const long long at = (long long)split * a.T * a.Hq + row;
+      const long long at = row * a.splits + split;
       a.part_o[at * D + d] = v;
       if (d == 0) a.part_ml[at] = make_float2(top, sum);
     } else {
-      const float r = sum == 0.f ? 0.f : v / sum;
-      if (a.out_f32) a.out_f32[row * D + d] = r;
-      else a.out_bf16[row * D + d] = (uint16_t)pack_bf16x2(r, 0.f);
-      if (d == 0 && a.lse) a.lse[row] = sum == 0.f ? -INFINITY : (top == -INFINITY ? 0.f : top) * 0.69314718055994531f + logf(sum);
+      write_out(a, row, D, d, v, top, sum);
     }
   }
 }
 
-// out = sum over the splits of 2^(m_i - m) O_i / sum of 2^(m_i - m) l_i, in split order.
-__global__ void attn_quant_join_kernel(const AttnQuantArgs a, int D) {
-  const long long rows = (long long)a.T * a.Hq;
-  const long long row = (long long)blockIdx.x * (blockDim.x / D) + threadIdx.x / D;
-  const int d = threadIdx.x % D;
-  if (row >= rows) return;
+// out = sum over the splits of 2^(m_i - m) O_i / sum of 2^(m_i - m) l_i.  A CTA a row; a warp
+// takes every kJoinWarps-th split and adds up its own in order, then the warps are added in
+// order; a lane holds D / 32 columns.  The O_i are asked for before the weights are known.
+constexpr int kJoinWarps = 8;
+constexpr int kJoinAhead = 10;
+constexpr int kJoinSplits = 148 * kAqMostCtas;  // most splits
+
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) attn_quant_join_kernel(const AttnQuantArgs a) {
+  constexpr int C = D / 32;
+  __shared__ float s_w[kJoinSplits], s_top[kJoinWarps], s_sum[kJoinWarps], s_v[kJoinWarps][D];
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const long long row = blockIdx.x;
+  const float* o = a.part_o + row * a.splits * D + lane * C;
+  float y[kJoinAhead][C];
+  auto ask = [&](int i0) {
+#pragma unroll
+    for (int k = 0; k < kJoinAhead; ++k) {
+      const int i = i0 + k * kJoinWarps;
+      if (i < a.splits) {
+        if constexpr (C == 4) {
+          const float4 x = *reinterpret_cast<const float4*>(o + (long long)i * D);
+          y[k][0] = x.x; y[k][1] = x.y; y[k][2] = x.z; y[k][3] = x.w;
+        } else {
+          const float2 x = *reinterpret_cast<const float2*>(o + (long long)i * D);
+          y[k][0] = x.x; y[k][1] = x.y;
+        }
+      }
+    }
+  };
+  ask(warp);
+  constexpr int kOwn = (kJoinSplits + kJoinWarps * 32 - 1) / (kJoinWarps * 32);
+  float2 ml[kOwn];
   float top = -INFINITY;
-  for (int i = 0; i < a.splits; ++i) top = fmaxf(top, a.part_ml[i * rows + row].x);
-  const float ref = top == -INFINITY ? 0.f : top;
-  float sum = 0.f, v = 0.f;
-  for (int i = 0; i < a.splits; ++i) {
-    const float2 ml = a.part_ml[i * rows + row];
-    const float w = exp2f(ml.x - ref);
-    // a NaN score leaves the maximum as it was: its sum counts whatever the maximum says
-    sum += ml.x == -INFINITY ? ml.y : ml.y * w;
-    v += a.part_o[(i * rows + row) * D + d] * w;
+#pragma unroll
+  for (int k = 0; k < kOwn; ++k) {
+    const int i = tid + k * kJoinWarps * 32;
+    ml[k] = i < a.splits ? a.part_ml[row * a.splits + i] : make_float2(-INFINITY, 0.f);
+    top = fmaxf(top, ml[k].x);
   }
-  const float r = sum == 0.f ? 0.f : v / sum;
-  if (a.out_f32) a.out_f32[row * D + d] = r;
-  else a.out_bf16[row * D + d] = (uint16_t)pack_bf16x2(r, 0.f);
-  if (d == 0 && a.lse) a.lse[row] = sum == 0.f ? -INFINITY : ref * 0.69314718055994531f + logf(sum);
+  top = warp_max(top);
+  if (lane == 0) s_top[warp] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, s_top[w]);
+  float sum = 0.f;
+#pragma unroll
+  for (int k = 0; k < kOwn; ++k) {
+    const int i = tid + k * kJoinWarps * 32;
+    const float weight = exp2f(ml[k].x - (top == -INFINITY ? 0.f : top));
+    if (i < a.splits) s_w[i] = weight;
+    // a NaN score leaves the maximum as it was: its sum counts all the same
+    sum += ml[k].x == -INFINITY ? ml[k].y : ml[k].y * weight;
+  }
+  sum = warp_sum(sum);
+  if (lane == 0) s_sum[warp] = sum;
+  __syncthreads();
+  float v[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) v[c] = 0.f;
+  for (int i0 = warp; i0 < a.splits; i0 += kJoinWarps * kJoinAhead) {
+    if (i0 != warp) ask(i0);
+#pragma unroll
+    for (int k = 0; k < kJoinAhead; ++k) {
+      const int i = i0 + k * kJoinWarps;
+      if (i < a.splits) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) v[c] += y[k][c] * s_w[i];
+      }
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < C; ++c) s_v[warp][lane * C + c] = v[c];
+  __syncthreads();
+  if (tid < D) {
+    float all = 0.f, x = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+      all += s_sum[w];
+      x += s_v[w][tid];
+    }
+    write_out(a, row, D, tid, x, top, all);
+  }
+}
+
+template <int FMT, int D, int GROUP, int NT, int HEADS>
+cudaError_t launch(AttnQuantArgs a, cudaStream_t s) {
+  a.splits = attn_quant_splits_of(ctas_per_sm<FMT, D, GROUP, NT>(), a.T, a.Hq, a.q.H, a.Kp, a.q.P_tok);
+  const int cols = a.T * (a.Hq / a.q.H);
+  const size_t ring = (size_t)kAqStages * Stage<FMT, D, GROUP>::kBytes;
+  const size_t join = (size_t)kAqWarps * 8 * NT * (D + 4) * sizeof(float), smem = ring > join ? ring : join;
+  if (smem > kDefaultSmemOptIn) {
+    const cudaError_t e = cudaFuncSetAttribute(attn_quant_kernel<FMT, D, GROUP, NT, HEADS>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  const dim3 grid((unsigned)(a.q.H / HEADS * a.splits), (cols + 8 * NT - 1) / (8 * NT));
+  attn_quant_kernel<FMT, D, GROUP, NT, HEADS><<<grid, kAqThreads, smem, s>>>(a);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || a.splits == 1) return e;
+  attn_quant_join_kernel<D><<<(unsigned)(a.T * a.Hq), kJoinWarps * 32, 0, s>>>(a);
+  return cudaGetLastError();
 }
 
 template <int FMT, int D, int GROUP>
-cudaError_t launch(const AttnQuantArgs& a, cudaStream_t s) {
-  const int cols = a.T * (a.Hq / a.q.H);
-  const unsigned x = (unsigned)(a.q.H * a.splits);
-  const size_t ring = (size_t)kAqWarps * kAqStages * Stage<FMT, D, GROUP>::kBytes;
-  auto go = [&](auto kernel, int nt) {
-    const size_t join = (size_t)8 * nt * D * sizeof(float), smem = ring > join ? ring : join;
-    if (smem > kDefaultSmemOptIn) {
-      const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-      if (e != cudaSuccess) return e;
-    }
-    kernel<<<dim3(x, (cols + 8 * nt - 1) / (8 * nt)), kAqThreads, smem, s>>>(a);
-    return cudaGetLastError();
-  };
-  cudaError_t e = cols <= 8 ? go(attn_quant_kernel<FMT, D, GROUP, 1>, 1) : go(attn_quant_kernel<FMT, D, GROUP, 2>, 2);
-  if (e != cudaSuccess || a.splits == 1) return e;
-  const int per = 256 / D;
-  const long long rows = (long long)a.T * a.Hq;
-  attn_quant_join_kernel<<<(unsigned)((rows + per - 1) / per), 256, 0, s>>>(a, D);
-  return cudaGetLastError();
+cudaError_t launch_heads(const AttnQuantArgs& a, cudaStream_t s) {
+  const int heads = attn_quant_heads(a.q.H);
+  if (a.T * (a.Hq / a.q.H) <= 8) {
+    if (heads == 4) return launch<FMT, D, GROUP, 1, 4>(a, s);
+    return heads == 2 ? launch<FMT, D, GROUP, 1, 2>(a, s) : launch<FMT, D, GROUP, 1, 1>(a, s);
+  }
+  if (heads == 4) return launch<FMT, D, GROUP, 2, 4>(a, s);
+  return heads == 2 ? launch<FMT, D, GROUP, 2, 2>(a, s) : launch<FMT, D, GROUP, 2, 1>(a, s);
 }
 
 template <int FMT>
 cudaError_t launch_fmt(const AttnQuantArgs& a, cudaStream_t s) {
   if (a.q.d == 128) {
-    if (a.q.group == 128) return launch<FMT, 128, 128>(a, s);
-    if (a.q.group == 64) return launch<FMT, 128, 64>(a, s);
-    return launch<FMT, 128, 32>(a, s);
+    if (a.q.group == 128) return launch_heads<FMT, 128, 128>(a, s);
+    if (a.q.group == 64) return launch_heads<FMT, 128, 64>(a, s);
+    return launch_heads<FMT, 128, 32>(a, s);
   }
-  if (a.q.group == 64) return launch<FMT, 64, 64>(a, s);
-  return launch<FMT, 64, 32>(a, s);
+  if (a.q.group == 64) return launch_heads<FMT, 64, 64>(a, s);
+  return launch_heads<FMT, 64, 32>(a, s);
 }
 
 }  // namespace
 
-// Splits of the rows: about kAqCtas CTAs on each SM in one wave, at least 4 tiles (one a
-// warp) to a split.
-int attn_quant_splits(int T, int Hq, int H, int d, int Kp, int P_tok) {
-  (void)d;
-  const int cols = T * (Hq / H);
-  const long long tiles = (long long)Kp * ((P_tok + 15) / 16);
-  const long long units = (long long)H * (cols <= 8 ? 1 : (cols + 15) / 16);
-  long long n = 148LL * (cols <= 8 ? kAqCtas : kAqCtasWide) / units;
-  const long long most = (tiles + kAqWarps - 1) / kAqWarps;
-  if (n > most) n = most;
-  return (int)(n < 1 ? 1 : n);
+int attn_quant_most_splits(int T, int Hq, int H, int Kp, int P_tok) {
+  return attn_quant_splits_of(kAqMostCtas, T, Hq, H, Kp, P_tok);
 }
 
 cudaError_t launch_attn_quant(const AttnQuantArgs& a, cudaStream_t s) {

@@ -221,12 +221,12 @@ struct AttnQuantArgs {
   float* out_f32;         // one of the two
   uint16_t* out_bf16;
   float* lse;             // may be NULL
-  int splits;
-  float* part_o;          // [splits][T * Hq][d], unused when splits == 1
-  float2* part_ml;        // [splits][T * Hq] (max in log2 units, sum)
+  int splits;             // set by the launcher, at most attn_quant_most_splits()
+  float* part_o;          // [T * Hq][splits][d], unused when splits == 1
+  float2* part_ml;        // [T * Hq][splits] (max in log2 units, sum)
   int* status;
 };
-int attn_quant_splits(int T, int Hq, int H, int d, int Kp, int P_tok);
+int attn_quant_most_splits(int T, int Hq, int H, int Kp, int P_tok);
 cudaError_t launch_attn_quant(const AttnQuantArgs& a, cudaStream_t s);
 
 // ---------------------------------------------------------------- waits.cu

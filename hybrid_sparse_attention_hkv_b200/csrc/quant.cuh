@@ -41,11 +41,11 @@ __device__ __forceinline__ void store_codes(void* p, const Codes8<FMT>& c) {
   else *static_cast<uint2*>(p) = make_uint2(c.w[0], c.w[1]);
 }
 
-// Two e4m3 bytes (low 16 bits) as a pair of halves (exact).
-__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t w) {
-  uint32_t h;
-  asm("{.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;}" : "=r"(h) : "r"(w));
-  return h;
+// Four e4m3 bytes as two pairs of halves (exact).
+__device__ __forceinline__ void e4m3x4_to_half2(uint32_t w, uint32_t& p0, uint32_t& p1) {
+  asm("{.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;}"
+      : "=r"(p0), "=r"(p1)
+      : "r"(w));
 }
 
 // code * scale of eight columns, in fp32.  Integers come out of the mantissa of 2^23 + u
@@ -55,11 +55,15 @@ template <int FMT>
 __device__ __forceinline__ void decode8(const Codes8<FMT>& c, float scale, float* f) {
   if constexpr (FMT == HKV_QUANT_E4M3) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t h = e4m3x2_to_half2(i & 1 ? c.w[i >> 1] >> 16 : c.w[i >> 1]);
-      const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h));
-      f[2 * i] = x.x * scale;
-      f[2 * i + 1] = x.y * scale;
+    for (int i = 0; i < 2; ++i) {
+      uint32_t h[2];
+      e4m3x4_to_half2(c.w[i], h[0], h[1]);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h[k]));
+        f[4 * i + 2 * k] = x.x * scale;
+        f[4 * i + 2 * k + 1] = x.y * scale;
+      }
     }
   } else if constexpr (FMT == HKV_QUANT_INT8) {
 #pragma unroll

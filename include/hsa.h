@@ -369,7 +369,9 @@ hsa_status_t hkv_store_residency(const hkv_store_t* st, int32_t* slot_of_page, i
 
 /* ------------------------------------------------- rotary positions ---- */
 
-/* Element types of the calls that take more than bf16. */
+/* The calls of this and the next section take d in {64, 128}, up to 16384 heads and, where
+ * they say so, element types other than bf16.  Their tensors need not follow the Lq, Lc
+ * rules above. */
 #define HSA_DTYPE_BF16 0
 #define HSA_DTYPE_FP16 1
 #define HSA_DTYPE_FP32 2

@@ -67,7 +67,8 @@ def test_page_size(lib, fmt, group, P_tok, H, d):
 
 
 @pytest.mark.parametrize("q,P_tok,H,d,code", [((3, 128), 8, 1, 128, 1), ((0, 16), 8, 1, 128, 2), ((0, 128), 8, 1, 64, 1),
-                                              ((0, 64), 0, 1, 64, 1), ((0, 64), 8, 0, 64, 1), ((0, 32), 8, 1, 96, 2)])
+                                              ((0, 64), 0, 1, 64, 1), ((0, 64), 8, 0, 64, 1), ((0, 32), 8, 1, 96, 2),
+                                              ((0, 64), 8, 16385, 64, 2)])
 def test_page_refusals(lib, q, P_tok, H, d, code):
     with pytest.raises(hsa.HsaError) as e:
         hsa.hkv_quant_page_size(hsa.make_quant(*q), P_tok, H, d)
@@ -103,6 +104,7 @@ def test_rope_refusals(lib, fn):
         (dict(rope=rope_struct(axes=(16, 16)), pos_stride=3), 1),
         (dict(qi=rows(data=None)), 1), (dict(qi=rows(data=0x10002)), 1), (dict(qi=rows(ts=132)), 1), (dict(qi=rows(hs=60)), 1),
         (dict(qi=rows(hs=56)), 1), (dict(qi=rows(ts=-128)), 1), (dict(qo=rows(ts=0)), 1), (dict(qo=rows(H=3)), 1), (dict(qi=rows(H=0)), 1),
+        (dict(qi=rows(H=16385), qo=rows(H=16385)), 2),
         (dict(ki=rows()), 1), (dict(ki=rows(), ko=rows(H=1)), 1), (dict(ki=rows(), ko=rows(ts=0)), 1),
     ]
     for kw, code in bad:
