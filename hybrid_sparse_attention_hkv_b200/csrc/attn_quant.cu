@@ -310,17 +310,24 @@ __global__ void __launch_bounds__(kAqThreads, (ctas_per_sm<FMT, D, GROUP, NT>())
     const int col = col0 + n * 8 + g;
     const bool on = col < cols;
     const uint16_t* src = a.Q + ((long long)(on ? col / share : 0) * a.Hq + h * share + (on ? col % share : 0)) * D;
-    float v[G * KS * 4];
+    float v[G * KS * 4];  // a group's codes of thread t are a run of GROUP / 4 columns
     float top = 0.f;
 #pragma unroll
-    for (int k = 0; k < G * KS; ++k)
+    for (int k = 0; k < G; ++k) {
+      uint32_t w[GROUP / 8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int d = (k / KS) * GROUP + t * (GROUP / 4) + code_at<FMT>(k % KS, i);
-        const float x = on ? __uint_as_float((uint32_t)__ldg(src + d) << 16) : 0.f;
-        v[4 * k + i] = x;
+      for (int i = 0; i < GROUP / 32; ++i) {
+        const uint4 x = on ? __ldg(reinterpret_cast<const uint4*>(src + k * GROUP + t * (GROUP / 4)) + i) : make_uint4(0, 0, 0, 0);
+        w[4 * i] = x.x; w[4 * i + 1] = x.y; w[4 * i + 2] = x.z; w[4 * i + 3] = x.w;
+      }
+#pragma unroll
+      for (int i = 0; i < KS * 4; ++i) {
+        const int c = code_at<FMT>(i / 4, i % 4);
+        const float x = c & 1 ? bf16_hi(w[c / 2]) : bf16_lo(w[c / 2]);
+        v[k * KS * 4 + i] = x;
         top = fmaxf(top, fabsf(x));
       }
+    }
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
     const float unit = pow2_below(top), inv = pow2_inverse(unit);
@@ -525,25 +532,31 @@ __global__ void __launch_bounds__(kAqThreads, (ctas_per_sm<FMT, D, GROUP, NT>())
       }
     }
   __syncthreads();
-  for (int i = tid; i < HEADS * COLS * D; i += kAqThreads) {
-    const int hw = i / (COLS * D), c = i / D % COLS, d = i % D, col = col0 + c;
+  for (int i = tid; i < HEADS * COLS * (D / 4); i += kAqThreads) {
+    const int hw = i / (COLS * (D / 4)), c = i / (D / 4) % COLS, d = i % (D / 4) * 4, col = col0 + c;
     if (col >= cols) continue;
     float top = -INFINITY;
 #pragma unroll
     for (int w = 0; w < kAqWarps; w += HEADS) top = fmaxf(top, s_m[w + hw][c]);
-    float sum = 0.f, v = 0.f;
+    float sum = 0.f;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kAqWarps; w += HEADS) {
       sum += top == -INFINITY ? s_l[w + hw][c] : s_l[w + hw][c] * exp2f(s_m[w + hw][c] - top);
-      v += s_o[((w + hw) * COLS + c) * kOPitch + d];
+      const float4 x = *reinterpret_cast<const float4*>(s_o + ((w + hw) * COLS + c) * kOPitch + d);
+      v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
     }
-    const long long row = (long long)(col / share) * a.Hq + (h0 + hw) * share + col % share;
+    const int token = col / share;
+    const long long row = (long long)token * a.Hq + (h0 + hw) * share + col - token * share;
     if (a.splits > 1) {
       const long long at = row * a.splits + split;
-      a.part_o[at * D + d] = v;
+      *reinterpret_cast<float4*>(a.part_o + at * D + d) = v;
       if (d == 0) a.part_ml[at] = make_float2(top, sum);
     } else {
-      write_out(a, row, D, d, v, top, sum);
+      write_out(a, row, D, d, v.x, top, sum);
+      write_out(a, row, D, d + 1, v.y, top, sum);
+      write_out(a, row, D, d + 2, v.z, top, sum);
+      write_out(a, row, D, d + 3, v.w, top, sum);
     }
   }
 }

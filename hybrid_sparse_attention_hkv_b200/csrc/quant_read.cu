@@ -199,19 +199,18 @@ __device__ __forceinline__ void read_rows(const ReadArgs& a, const ReadArgs::Par
   cp_async_wait<0>();
   if constexpr (POOL) {
     __syncthreads();  // the last cos and sin have been read
-    for (int p = 0; p < phases; ++p) {
-      if (active && phase == p) {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          float& s = smem[(item / J) * D + (k < 8 ? c.lo * 8 + k : c.hi * 8 + k - 8)];
-          s = p == 0 ? acc[k] : s + acc[k];
-        }
-      }
-      __syncthreads();
-    }
+    for (int k = 0; k < 16; ++k) smem[k * threads + tid] = acc[k];
+    __syncthreads();
     const float inv = 1.f / (float)rows;
     float* mean = a.kbar128 + (blk * q.H + h0) * D;
-    for (int v = tid; v < items / J * D; v += threads) mean[v] = smem[v] * inv;
+    for (int v = tid; v < items * 16; v += threads) {
+      const int k = v / items, it = v - k * items;
+      const ChunkPair cc = chunk_pair<J, ROPE>(a.r, it % J);
+      float sum = smem[k * threads + it];
+      for (int p = 1; p < phases; ++p) sum += smem[k * threads + p * (part.slab * J) + it];
+      mean[it / J * D + (k < 8 ? cc.lo * 8 + k : cc.hi * 8 + k - 8)] = sum * inv;
+    }
   }
 }
 
@@ -224,11 +223,13 @@ __global__ void __launch_bounds__(kReadThreads, kReadCtas) gather_quant_kernel(c
     read_rows<FMT, J, kRopeNone, false, kReadRows>(a, a.v, blockIdx.x - a.k.ctas, a.page_v, a.Vc, smem);
 }
 
-// The shares of CTAs of `rows` rows.
+// The shares of CTAs of `rows` rows: the widest slabs, or narrower ones (and so more rows at
+// once, each in fewer rounds) where a short cache leaves SMs idle.
 template <int J>
 ReadArgs::Part read_part(const ReadArgs& a, int rows) {
   ReadArgs::Part p;
   p.slabs = (a.q.H * J + kReadThreads - 1) / kReadThreads;
+  while (p.slabs < a.q.H && (a.Lc + rows - 1) / rows * p.slabs < 148) p.slabs = min(2 * p.slabs, a.q.H);
   p.slab = (a.q.H + p.slabs - 1) / p.slabs;
   p.slabs = (a.q.H + p.slab - 1) / p.slab;
   p.phases = kReadThreads / (p.slab * J);
@@ -244,7 +245,7 @@ cudaError_t launch_read(ReadArgs& a, cudaStream_t s) {
   const int need = max(a.k.slab * a.k.phases, a.v.slab * a.v.phases) * J;
   const int threads = max(8 * J, (need + 31) / 32 * 32);  // 8 J: the cos and sin of a row
   size_t smem = ROPE != kRopeNone ? (size_t)(POOL ? kReadBatch : kReadRows) * 8 * J * sizeof(float2) : 0;
-  const size_t pool = POOL ? (size_t)a.k.slab * J * 16 * sizeof(float) : 0;
+  const size_t pool = POOL ? (size_t)threads * 16 * sizeof(float) : 0;
   if (pool > smem) smem = pool;
   a.ring_offset = (int)smem;
   smem += (size_t)kReadRing * threads * ReadSlot<FMT>::kBytes;
