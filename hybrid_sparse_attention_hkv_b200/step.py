@@ -11,7 +11,7 @@ from __future__ import annotations
 
 import torch
 
-from . import (FWD_SELECTED, SelectionBuffers, hkv_block_means_from_pages, hkv_gather,
+from . import (FWD_SELECTED, SelectionBuffers, hkv_block_means_from_pages, hkv_gather, hkv_gather_quant,
                hkv_page_block_sums, hkv_page_summary, hkv_select_pages, hkv_select_prompt,
                hsa_block_select, hsa_forward, hsa_forward_ex, hsa_forward_reuse, hsa_prepare_history,
                hsa_workspace_size, make_config)
@@ -28,10 +28,13 @@ def page_pointers(pages: torch.Tensor) -> torch.Tensor:
 
 class HkvHsaStep:
     def __init__(self, H, d, Lq, P_tok, NP, Kp, rank, page_k_ptrs, page_v_ptrs, out_dtype=torch.float32,
-                 scale=0.0, device="cuda", store=None):
+                 scale=0.0, device="cuda", store=None, quant=None, rope=None, pos=None):
         """page_k_ptrs / page_v_ptrs: device int64 page tables read by the gather.  With a
         tiered page store (`store`, a PageStore), pass its tables: every retrieval is
-        then followed by the store's fetch (the selected pages made resident in HBM)."""
+        then followed by the store's fetch (the selected pages made resident in HBM).
+        quant (make_quant): the pages are quantised (with `store`, a QuantPageStore).
+        rope, pos (make_rope; int32 [n_axes, Kp * P_tok]): their keys are rotated as they
+        are read, to their places in the active cache; Q and Kq come rotated (hsa_rope)."""
         self.H, self.d, self.Lq, self.P_tok, self.NP, self.Kp, self.rank = H, d, Lq, P_tok, NP, Kp, rank
         self.store = store
         self.Lc = Kp * P_tok
@@ -51,7 +54,12 @@ class HkvHsaStep:
         self.out = torch.empty(Lq, H, d, dtype=out_dtype, device=dev)
         # Pages of a multiple of 64 rows keep their 64-row key sums (from the seal): the
         # block selection then runs from them while the gather copies, on its own stream.
-        self.early = P_tok % 64 == 0
+        # Quantised pages are read with their block means instead: the sums of the sealed
+        # keys are not those of the keys as they are read.
+        self.quant, self.rope, self.pos = quant, rope, pos
+        if rope is not None and quant is None:
+            raise ValueError("keys are rotated on the way from quantised pages only (quant is None)")
+        self.early = P_tok % 64 == 0 and quant is None
         self.sums64 = torch.zeros(NP, P_tok // 64, H, d, dtype=torch.float32, device=dev) if self.early else None
         self.gather_stream = torch.cuda.Stream(device=dev) if self.early else None
         self.ev_sel = torch.cuda.Event()
@@ -70,6 +78,15 @@ class HkvHsaStep:
         hkv_select_pages(self.kbar_pages, Q, self.Kp, self.sel, self.ws, self.scores, cand)
         return self.sel
 
+    def _gather(self):
+        """The selected pages into the active cache, with its block means."""
+        if self.quant is not None:
+            hkv_gather_quant(self.quant, self.page_k_ptrs, self.page_v_ptrs, self.sel, self.Kp, self.P_tok, self.H, self.d,
+                             self.Kc, self.Vc, self.ws, self.kbar128, self.rope, self.pos)
+        else:
+            hkv_gather(self.page_k_ptrs, self.page_v_ptrs, self.sel, self.Kp, self.P_tok, self.H, self.d, self.Kc, self.Vc,
+                       self.ws, self.kbar128)
+
     def __call__(self, Q, Kq, Vq, tau, gate_logit, E, F, e_cur=None, e_seg=None, seg_begin=None,
                  ef_head_stride=0, out=None):
         """One step on the current stream; the result goes to `out` (same shape and
@@ -83,8 +100,7 @@ class HkvHsaStep:
         if self.store is not None:
             self.store.fetch(self.sel, self.ws)
         if not self.early:
-            hkv_gather(self.page_k_ptrs, self.page_v_ptrs, self.sel, self.Kp, self.P_tok, self.H, self.d,
-                       self.Kc, self.Vc, self.ws, self.kbar128)
+            self._gather()
             hsa_forward(self.cfg, Q, self.Kc, self.Vc, Kq, Vq, tau, gate_logit, E, F, dst, self.ws,
                         self.kbar128, self.selection, ef_head_stride)
             return dst
@@ -115,8 +131,7 @@ class HkvHsaStep:
         self._retrieve(Q, cand)
         if self.store is not None:
             self.store.fetch(self.sel, self.ws)
-        hkv_gather(self.page_k_ptrs, self.page_v_ptrs, self.sel, self.Kp, self.P_tok, self.H, self.d,
-                   self.Kc, self.Vc, self.ws, self.kbar128)
+        self._gather()
         hsa_prepare_history(self.cfg, self.Kc, self.Vc, E, F, self.ws, ef_head_stride)
 
     def denoise_step(self, Q, Kq, Vq, tau, gate_logit, E, F, ef_head_stride=0, out=None):

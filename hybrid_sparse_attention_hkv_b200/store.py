@@ -11,7 +11,8 @@ import ctypes
 
 import torch
 
-from . import StoreDesc, _check, _p, _stream, load_library
+from . import (Quant, StoreDesc, _check, _p, _refuse, _stream, hkv_attn_quant, hkv_gather_quant, hkv_page_summary,
+               hkv_quant_page_size, hkv_quant_rows, load_library)
 
 
 class MappedHostMemory:
@@ -92,3 +93,41 @@ class PageStore:
             for h in self.host:
                 h.close()
         self.host = None
+
+
+class QuantPageStore(PageStore):
+    """A page store whose pages are quantised: half or a quarter of the host tier, of the HBM slots and of the host link's
+    traffic of bf16 pages.  The residency calls (fetch, prefetch, residency) are PageStore's: to them a page is a block of
+    bytes, passed as page_bytes / 1024 rows of 4 x 128 bf16 elements.  Rows are written to the host tier; a page is fetched
+    once its rows are written (a slot keeps the copy it was given)."""
+
+    def __init__(self, quant: Quant, NP: int, S: int, P_tok: int, H: int, d: int, host=None, stream=None):
+        self.quant, self.rows, self.heads, self.head_dim = quant, P_tok, H, d
+        self.page_bytes, self.scale_offset = hkv_quant_page_size(quant, P_tok, H, d)
+        super().__init__(NP, S, self.page_bytes // 1024, 4, 128, host, stream)
+        at = torch.arange(NP, dtype=torch.int64) * self.page_bytes
+        self.host_tables = tuple((at + h.dev_ptr).to(self.slot_k.device) for h in self.host)
+
+    def write(self, K, V, first_row: int, ws, first_row_dev=None, rope=None, pos=None, stream=None):
+        """Append rows K, V [T, H, d] at history row first_row (+ first_row_dev): hkv_quant_rows into the host tier."""
+        hkv_quant_rows(self.quant, K, V, *self.host_tables, self.rows, first_row, ws, first_row_dev, rope, pos, stream)
+
+    def seal(self, page: int, K_rows, V_rows, kbar_out, ws, rope=None, pos=None, stream=None):
+        """Write the rows of page `page` and its summary kbar_out (the mean of K_rows, bf16, before any rotation)."""
+        if K_rows.shape != (self.rows, self.heads, self.head_dim) or K_rows.dtype != torch.bfloat16 or not K_rows.is_contiguous():
+            _refuse("QuantPageStore.seal", f"K_rows is {list(K_rows.shape)} {K_rows.dtype}: a contiguous bfloat16 "
+                                           f"[{self.rows}, {self.heads}, {self.head_dim}] wanted")
+        if not 0 <= page < self.NP:
+            _refuse("QuantPageStore.seal", f"page {page} outside [0, {self.NP})")
+        self.write(K_rows, V_rows, page * self.rows, ws, rope=rope, pos=pos, stream=stream)
+        hkv_page_summary(K_rows, kbar_out, ws, stream)
+
+    def gather(self, sel, Kc, Vc, ws, kbar128=None, rope=None, pos=None, stream=None):
+        """hkv_gather_quant of the pages `sel` (int32 device tensor), from their slots or the host tier."""
+        hkv_gather_quant(self.quant, *self.page_tables(), sel, sel.numel(), self.rows, self.heads, self.head_dim, Kc, Vc, ws,
+                         kbar128, rope, pos, stream)
+
+    def attend(self, Q, sel, out, lse, ws, n_rows=None, scale=0.0, stream=None):
+        """hkv_attn_quant of a few queries over the pages `sel`."""
+        hkv_attn_quant(self.quant, Q, *self.page_tables(), sel, sel.numel(), self.rows, self.heads, out, lse, ws, n_rows, scale,
+                       stream)
