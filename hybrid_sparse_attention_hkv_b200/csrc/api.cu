@@ -1144,6 +1144,8 @@ hsa_status_t hkv_gather_quant(const hkv_quant_t* q, const void* const* page_k, c
   TRY(quant_args(fn, q, P_tok, H, d, &a));
   if (NP < 1) return fail(HSA_ERR_INVALID_ARG, "%s: NP = %d must be >= 1", fn, NP);
   if (Kp < 1 || Kp > NP) return fail(HSA_ERR_INVALID_ARG, "%s: Kp = %d must be in [1, NP]", fn, Kp);
+  if ((long long)Kp * P_tok > 0x7fffffffLL)
+    return fail(HSA_ERR_UNSUPPORTED, "%s: Kp * P_tok = %lld rows exceed 2^31 - 1", fn, (long long)Kp * P_tok);
   if (!page_k || !page_v || !sel) return fail(HSA_ERR_INVALID_ARG, "%s: NULL page table or selection", fn);
   REQUIRE_PTR(Kc);
   REQUIRE_PTR(Vc);

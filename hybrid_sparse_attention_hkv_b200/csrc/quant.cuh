@@ -49,7 +49,7 @@ __device__ __forceinline__ void e4m3x4_to_half2(uint32_t w, uint32_t& p0, uint32
 }
 
 // code * scale of eight columns, in fp32.  Integers come out of the mantissa of 2^23 + u
-// (u the code plus 128 or 8, exact), which costs a byte permute and an add where an
+// (u the code plus 128 or 8, exact), which costs a byte permute or a mask and an add where an
 // integer conversion would go through the quarter-rate pipe.
 template <int FMT>
 __device__ __forceinline__ void decode8(const Codes8<FMT>& c, float scale, float* f) {
@@ -72,9 +72,14 @@ __device__ __forceinline__ void decode8(const Codes8<FMT>& c, float scale, float
       f[i] = (__uint_as_float(u) - 8388736.f) * scale;
     }
   } else {
-    const uint32_t w = c.w[0] ^ 0x88888888u;
+    // nibble i left where it is: 2^23 + 16^i (n + 8), taken off and scaled by scale / 16^i
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = (__uint_as_float(((w >> (4 * i)) & 15u) | 0x4B000000u) - 8388616.f) * scale;
+    for (int i = 0; i < 8; ++i) {
+      const int at = i < 5 ? 4 * i : 4 * i - 20;
+      const uint32_t w = i < 5 ? c.w[0] : c.w[0] >> 20;
+      const float x = __uint_as_float((w & (15u << at)) ^ (0x4B000000u | (8u << at)));
+      f[i] = (x - (8388608.f + (float)(8u << at))) * (scale * (1.f / (float)(1u << at)));
+    }
   }
 }
 

@@ -24,7 +24,8 @@ namespace {
 constexpr int kReadCtas = 3;  // on an SM
 constexpr int kReadRing = 4;
 constexpr int kReadThreads = 320;
-constexpr int kReadRows = 16;
+constexpr int kReadRows = 16;   // of a CTA, or more:
+constexpr int kReadRounds = 8;
 constexpr int kReadBatch = 32;  // rows whose cos and sin are held at once
 
 struct ReadArgs {
@@ -34,10 +35,10 @@ struct ReadArgs {
   const void* const* page_v;
   int NP;
   const int32_t* sel;
-  long long Lc;
+  int Lc;
   struct Part {        // how K's, or V's, rows are shared out to CTAs
     int slab, slabs;   // heads of a CTA, and how many such slabs there are (the fastest index)
-    int phases;
+    int phases, rows;  // rows of a CTA, and those that it works on at once
     unsigned ctas;
   } k, v;
   int ring_offset;
@@ -58,10 +59,10 @@ struct ReadCursor {
   int left;        // rows from there to its page's end
   int slot, phases;
 
-  __device__ __forceinline__ void seek(const ReadArgs& a, const void* const* table, long long r0, int h) {
+  __device__ __forceinline__ void seek(const ReadArgs& a, const void* const* table, int r0, int h) {
     constexpr int D = 16 * J;
-    slot = (int)((r0 + row) / a.q.P_tok);
-    const int t = (int)(r0 + row - (long long)slot * a.q.P_tok);
+    slot = (unsigned)(r0 + row) / (unsigned)a.q.P_tok;
+    const int t = r0 + row - slot * a.q.P_tok;
     left = a.q.P_tok - t;
     const int p = a.sel[slot];
     const char* base = (p >= 0 && p < a.NP) ? static_cast<const char*>(table[p]) : nullptr;
@@ -75,7 +76,7 @@ struct ReadCursor {
     }
   }
   // The step to the next row; false at the CTA's end.
-  __device__ __forceinline__ bool next(const ReadArgs& a, const void* const* table, long long r0, int h, int rows) {
+  __device__ __forceinline__ bool next(const ReadArgs& a, const void* const* table, int r0, int h, int rows) {
     row += phases;
     if (row >= rows) return false;
     left -= phases;
@@ -100,13 +101,13 @@ struct ReadSlot {
   static constexpr int kBytes = 2 * kCodeBytes + 8;    // lo and hi chunk, their two scales
 };
 
-template <int FMT, int J, int ROPE, bool POOL, int ROWS>
+template <int FMT, int J, int ROPE, bool POOL>
 __device__ __forceinline__ void read_rows(const ReadArgs& a, const ReadArgs::Part& part, unsigned cta,
                                           const void* const* table, uint16_t* dst, float* smem) {
   constexpr int D = 16 * J, BITS = code_bits<FMT>();
   const QuantArgs& q = a.q;
-  const long long blk = cta / part.slabs, r0 = blk * ROWS;
-  const int rows = (int)min((long long)ROWS, a.Lc - r0);
+  const int blk = cta / (unsigned)part.slabs, r0 = blk * part.rows;
+  const int rows = min(part.rows, a.Lc - r0);
   const int h0 = (int)(cta - blk * part.slabs) * part.slab;
   const int items = min(part.slab, q.H - h0) * J, phases = part.phases;
   const int tid = threadIdx.x;
@@ -150,12 +151,12 @@ __device__ __forceinline__ void read_rows(const ReadArgs& a, const ReadArgs::Par
   };
 #pragma unroll
   for (int s = 0; s < kReadRing - 1; ++s) ask(s);
-  uint16_t* out = dst + ((r0 + phase) * q.H + h) * D;
+  uint16_t* out = dst + ((long long)(r0 + phase) * q.H + h) * D;
   const long long out_step = (long long)phases * q.H * D;
   int slot = 0, i = phase;
   for (int b0 = 0; b0 < rows; b0 += kReadBatch) {
     if constexpr (ROPE != kRopeNone) {
-      if (ROWS > kReadBatch && b0) __syncthreads();  // the last rows' cos and sin have been read
+      if (b0) __syncthreads();  // the last rows' cos and sin have been read
       rope_table<J, ROPE>(a.r, r0 + b0, min(kReadBatch, rows - b0), reinterpret_cast<float4*>(smem), tid, threads);
       __syncthreads();
     }
@@ -203,7 +204,7 @@ __device__ __forceinline__ void read_rows(const ReadArgs& a, const ReadArgs::Par
     for (int k = 0; k < 16; ++k) smem[k * threads + tid] = acc[k];
     __syncthreads();
     const float inv = 1.f / (float)rows;
-    float* mean = a.kbar128 + (blk * q.H + h0) * D;
+    float* mean = a.kbar128 + ((long long)blk * q.H + h0) * D;
     for (int v = tid; v < items * 16; v += threads) {
       const int k = v / items, it = v - k * items;
       const ChunkPair cc = chunk_pair<J, ROPE>(a.r, it % J);
@@ -214,37 +215,45 @@ __device__ __forceinline__ void read_rows(const ReadArgs& a, const ReadArgs::Par
   }
 }
 
+// (Both members of eight pairs and their sums at once are too much for 64 registers: with two
+// CTAs an SM and no spills the half layout's block means take 276 us where three take 300.)
 template <int FMT, int J, int ROPE, bool POOL>
-__global__ void __launch_bounds__(kReadThreads, kReadCtas) gather_quant_kernel(const ReadArgs a) {
+__global__ void __launch_bounds__(kReadThreads, ROPE == kRopeHalf && POOL ? 2 : kReadCtas) gather_quant_kernel(const ReadArgs a) {
   extern __shared__ __align__(16) float smem[];
   if (blockIdx.x < a.k.ctas)
-    read_rows<FMT, J, ROPE, POOL, POOL ? 128 : kReadRows>(a, a.k, blockIdx.x, a.page_k, a.Kc, smem);
+    read_rows<FMT, J, ROPE, POOL>(a, a.k, blockIdx.x, a.page_k, a.Kc, smem);
   else
-    read_rows<FMT, J, kRopeNone, false, kReadRows>(a, a.v, blockIdx.x - a.k.ctas, a.page_v, a.Vc, smem);
+    read_rows<FMT, J, kRopeNone, false>(a, a.v, blockIdx.x - a.k.ctas, a.page_v, a.Vc, smem);
 }
 
-// The shares of CTAs of `rows` rows: the widest slabs, or narrower ones (and so more rows at
-// once, each in fewer rounds) where a short cache leaves SMs idle.
+// The shares of CTAs of 128 rows (for the block means), or of about 16, in eight rounds or more,
+// fewer where a short cache leaves SMs idle.  Slabs are as wide as they can be, or narrower (and
+// so more rows at once) where a short cache leaves SMs idle all the same.
 template <int J>
-ReadArgs::Part read_part(const ReadArgs& a, int rows) {
+ReadArgs::Part read_part(const ReadArgs& a, bool pool) {
   ReadArgs::Part p;
   p.slabs = (a.q.H * J + kReadThreads - 1) / kReadThreads;
-  while (p.slabs < a.q.H && (a.Lc + rows - 1) / rows * p.slabs < 148) p.slabs = min(2 * p.slabs, a.q.H);
+  p.slab = (a.q.H + p.slabs - 1) / p.slabs;
+  p.phases = kReadThreads / (p.slab * J);
+  int rounds = p.phases < kReadRows / kReadRounds ? kReadRows / p.phases : kReadRounds;
+  while (rounds > 1 && a.Lc / (p.phases * rounds) * p.slabs < 2 * 148) --rounds;
+  p.rows = pool ? 128 : p.phases * rounds;
+  while (p.slabs < a.q.H && ((a.Lc - 1) / p.rows + 1) * p.slabs < 148) p.slabs = min(2 * p.slabs, a.q.H);
   p.slab = (a.q.H + p.slabs - 1) / p.slabs;
   p.slabs = (a.q.H + p.slab - 1) / p.slab;
   p.phases = kReadThreads / (p.slab * J);
-  if (p.phases > rows) p.phases = rows;
-  p.ctas = (unsigned)((a.Lc + rows - 1) / rows * p.slabs);
+  if (p.phases > p.rows) p.phases = p.rows;
+  p.ctas = (unsigned)((a.Lc - 1) / p.rows + 1) * p.slabs;
   return p;
 }
 
 template <int FMT, int J, int ROPE, bool POOL>
 cudaError_t launch_read(ReadArgs& a, cudaStream_t s) {
-  a.k = read_part<J>(a, POOL ? 128 : kReadRows);
-  a.v = read_part<J>(a, kReadRows);
+    a.k = read_part<J>(a, POOL);
+  a.v = read_part<J>(a, false);
   const int need = max(a.k.slab * a.k.phases, a.v.slab * a.v.phases) * J;
   const int threads = max(8 * J, (need + 31) / 32 * 32);  // 8 J: the cos and sin of a row
-  size_t smem = ROPE != kRopeNone ? (size_t)(POOL ? kReadBatch : kReadRows) * 8 * J * sizeof(float2) : 0;
+  size_t smem = ROPE != kRopeNone ? (size_t)kReadBatch * 8 * J * sizeof(float2) : 0;
   const size_t pool = POOL ? (size_t)threads * 16 * sizeof(float) : 0;
   if (pool > smem) smem = pool;
   a.ring_offset = (int)smem;
@@ -276,7 +285,7 @@ cudaError_t launch_read_head(ReadArgs& a, cudaStream_t s) {
 cudaError_t launch_gather_quant(const QuantArgs& q, const RopeArgs& r, const void* const* page_k,
                                 const void* const* page_v, int NP, const int32_t* sel, int Kp, uint16_t* Kc,
                                 uint16_t* Vc, float* kbar128, int* status, cudaStream_t s) {
-  ReadArgs a{q, r, page_k, page_v, NP, sel, (long long)Kp * q.P_tok, {}, {}, 0, Kc, Vc, kbar128, status};
+  ReadArgs a{q, r, page_k, page_v, NP, sel, Kp * q.P_tok, {}, {}, 0, Kc, Vc, kbar128, status};
   switch (q.format) {
     case HKV_QUANT_E4M3: return launch_read_head<HKV_QUANT_E4M3>(a, s);
     case HKV_QUANT_INT8: return launch_read_head<HKV_QUANT_INT8>(a, s);

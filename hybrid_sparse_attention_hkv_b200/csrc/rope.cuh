@@ -46,16 +46,29 @@ __device__ __forceinline__ ChunkPair chunk_pair(const RopeArgs& r, int j) {
   return c;
 }
 
-// (mscale cos, mscale sin) of a pair at a position.  The angle in turns, pos * inv_freq / 2 pi,
-// is formed and reduced to [-1/2, 1/2] in fp64: its error is about 2^-52 of the turns made
-// (2^-21 of a turn after 2^31 of them), and the fp32 rounding behind the reduction costs at
-// most 2^-26 of a turn.  sign = -1 turns backward (the gradient).
-__device__ __forceinline__ float2 rope_cos_sin(const RopeArgs& r, int pos, double turns_per_step) {
-  double turns = (double)pos * turns_per_step;
-  turns -= rint(turns);
-  float s, c;
-  sincospif((float)(2.0 * turns), &s, &c);
-  return make_float2(c * r.mscale, s * r.mscale * r.sign);
+// (mscale cos, mscale sin) of a pair at a position.  The angle in quarter turns,
+// pos * inv_freq * 2 / pi, is formed and reduced to [-1/2, 1/2] in fp64 (adding 1.5 * 2^52
+// rounds it to an integer, whose low bits name the quarter): its error is about 2^-52 of the
+// turns made (2^-21 of a turn after 2^31 of them).  The rest, at most pi / 4, goes through the
+// Taylor series of sin (to the 9th power, error below 2^-29) and cos (10th, 2^-33) in fp32:
+// two roundings of the angle and those of the series leave an error below 2^-22.  sign = -1
+// turns backward (the gradient).
+__device__ __forceinline__ float2 rope_cos_sin(const RopeArgs& r, int pos, double quarters_per_step) {
+  const double quarters = (double)pos * quarters_per_step, shifted = quarters + 6755399441055744.0;
+  const int q = __double2loint(shifted);
+  // (clamped: beyond 2^51 quarter turns nothing is left of the angle, and the series is not to leave its range)
+  const float rest = fminf(fmaxf((float)(quarters - (shifted - 6755399441055744.0)), -0.5f), 0.5f);
+  const float a = rest * 1.57079632679489662f, x = a * a;
+  float s = fmaf(x, 1.f / 362880, -1.f / 5040), c = fmaf(x, -1.f / 3628800, 1.f / 40320);
+  s = fmaf(x, s, 1.f / 120);
+  c = fmaf(x, c, -1.f / 720);
+  s = fmaf(x, s, -1.f / 6);
+  c = fmaf(x, c, 1.f / 24);
+  s = fmaf(a * x, s, a);
+  c = fmaf(x, c, -0.5f);
+  c = fmaf(x, c, 1.f);
+  const float cc = q & 1 ? s : c, ss = q & 1 ? c : s;
+  return make_float2((q + 1) & 2 ? -cc * r.mscale : cc * r.mscale, (q & 2 ? -ss : ss) * (r.mscale * r.sign));
 }
 
 // The cos and sin of `rows` tokens from t0 on, in the order the threads read them: for each
@@ -72,9 +85,9 @@ __device__ __forceinline__ void rope_table(const RopeArgs& r, long long t0, int 
   if (tid >= rows_at_once * 8 * J || !(i < 4 ? c.rot_lo : c.rot_hi)) return;
   const int p = ROPE == kRopeHalf ? 8 * c.lo + i : 4 * (i < 4 ? c.lo : c.hi) + (i & 3);
   const int32_t* pos = r.pos + ((p >= r.end0) + (p >= r.end1)) * r.pos_stride + t0;
-  const double turns_per_step = __ldg(r.inv_freq + p) * 0.15915494309189533577;  // 1 / (2 pi)
+  const double quarters_per_step = __ldg(r.inv_freq + p) * 0.63661977236758134308;  // 2 / pi
   for (int row = tid / (8 * J); row < rows; row += rows_at_once)
-    reinterpret_cast<float2*>(table)[row * 8 * J + slot] = rope_cos_sin(r, __ldg(pos + row), turns_per_step);
+    reinterpret_cast<float2*>(table)[row * 8 * J + slot] = rope_cos_sin(r, __ldg(pos + row), quarters_per_step);
 }
 
 // Rotate a thread's two chunks in fp32; row: the table's row of its token.

@@ -160,7 +160,7 @@ def test_gather_quant_refusals(lib):
     bad = [
         (dict(q=(-1, 64)), 1), (dict(q=(1, 128)), 1), (dict(pk=None), 1), (dict(pv=None), 1), (dict(NP=0), 1), (dict(sel=None), 1),
         (dict(Kp=0), 1), (dict(Kp=5), 1), (dict(P_tok=0), 1), (dict(H=0), 1), (dict(d=256), 2), (dict(Kc=None), 1),
-        (dict(Vc=P(0x10008)), 1), (dict(kb=P(MIS)), 1), (dict(rope=rope_struct()), 1),
+        (dict(Vc=P(0x10008)), 1), (dict(kb=P(MIS)), 1), (dict(P_tok=2 ** 30), 2), (dict(rope=rope_struct()), 1),
         (dict(rope=rope_struct(axes=(16, 16)), pos=P(A), pos_stride=15), 1), (dict(ws=None), 3), (dict(wsb=0), 3),
     ]
     for kw, code in bad:
