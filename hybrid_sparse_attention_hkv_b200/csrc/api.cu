@@ -994,7 +994,11 @@ static hsa_status_t rows_args(const char* fn, const char* what, const hsa_rows_t
   if (x->token_stride % unit != 0 || x->head_stride % unit != 0)
     return fail(HSA_ERR_INVALID_ARG, "%s: %s: strides %lld, %lld are not multiples of 16 bytes", fn, what, x->token_stride,
                 x->head_stride);
-  if (x->head_stride < d || x->token_stride < 0 || (out && T > 1 && x->token_stride < d))
+  // elements of an output are one to an address: tokens lie between a head's rows, or heads between a token's
+  const bool apart = T <= 1 || x->H == 1 ? x->token_stride >= d || T <= 1
+                                         : x->token_stride >= d && (x->token_stride >= (x->H - 1) * x->head_stride + d ||
+                                                                        x->head_stride >= (T - 1LL) * x->token_stride + d);
+  if (x->head_stride < d || x->token_stride < 0 || (out && !apart))
     return fail(HSA_ERR_INVALID_ARG, "%s: %s: strides %lld, %lld overlap (d = %d)", fn, what, x->token_stride,
                 x->head_stride, d);
   r->data = x->data;
@@ -1166,6 +1170,8 @@ static hsa_status_t attn_quant_layout(const char* fn, int T, int Hq, int H, int 
   TRY(check_many_heads(fn, H));
   TRY(check_many_heads(fn, Hq));
   if (Hq < 1 || Hq % H != 0) return fail(HSA_ERR_INVALID_ARG, "%s: Hq = %d is not a multiple of H = %d", fn, Hq, H);
+  if ((long long)T * (Hq / H) > 65535)
+    return fail(HSA_ERR_UNSUPPORTED, "%s: %lld queries to a key head (supported: up to 65535)", fn, (long long)T * (Hq / H));
   if (Kp < 1 || P_tok < 1) return fail(HSA_ERR_INVALID_ARG, "%s: Kp = %d, P_tok = %d must be >= 1", fn, Kp, P_tok);
   if ((long long)Kp * P_tok > 0x7fffffffLL)
     return fail(HSA_ERR_UNSUPPORTED, "%s: Kp * P_tok = %lld rows exceed 2^31 - 1", fn, (long long)Kp * P_tok);

@@ -152,7 +152,8 @@ hsa_status_t hsa_thread_release(void);
  * GPU (failure detection; the pages have no counterpart).  Sets the calling
  * thread's fault kind until it is set back to HSA_FAULT_NONE:
  *   HSA_FAULT_ARG        the configuration check of every entry point that takes
- *                        an hsa_config_t fails: HSA_ERR_INVALID_ARG;
+ *                        an hsa_config_t (or an hkv_quant_t) fails:
+ *                        HSA_ERR_INVALID_ARG;
  *   HSA_FAULT_WORKSPACE  the workspace check of every entry point that takes a
  *                        workspace fails: HSA_ERR_WORKSPACE;
  *   HSA_FAULT_LAUNCH     every entry point that launches kernels fails at its
@@ -400,7 +401,8 @@ typedef struct {
 /* One tensor of token rows [T, H, d] inside a larger one: element (t, h, c) is at
  * data[t * token_stride + h * head_stride + c].  data is 16-byte aligned and the
  * strides (in elements) are multiples of 16 bytes, head_stride >= d and
- * token_stride >= 0 (0 broadcasts one row; not for outputs). */
+ * token_stride >= 0 (0 broadcasts one row).  The elements of an output are each at an
+ * address of their own. */
 typedef struct {
   void* data;
   int H;
@@ -434,7 +436,8 @@ hsa_status_t hsa_rope(const hsa_rope_t* rope, const int32_t* pos, long long pos_
                       const hsa_rows_t* k_out, hsa_stream_t stream);
 
 /* The gradient of hsa_rope: given dL/dy in q_in / k_in, writes dL/dx = mscale R(-theta)
- * dL/dy to q_out / k_out (the columns from rot_dim on are copied). */
+ * dL/dy to q_out / k_out (the columns from rot_dim on are copied).  Where hsa_rope read
+ * one row for many tokens (token_stride 0), that row's gradient is the sum of theirs. */
 hsa_status_t hsa_rope_bwd(const hsa_rope_t* rope, const int32_t* pos, long long pos_stride, int T, int d, int dtype,
                           const hsa_rows_t* q_in, const hsa_rows_t* q_out, const hsa_rows_t* k_in,
                           const hsa_rows_t* k_out, hsa_stream_t stream);

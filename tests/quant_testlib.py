@@ -6,8 +6,9 @@ import torch
 
 QMAX = {0: 448.0, 1: 127.0, 2: 7.0}
 HALF_STEP = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11, torch.float32: 2.0 ** -24}
-# Rotating in fp32 (rope.cuh): the reduced angle is rounded once (2^-24 of at most pi: below 2^-22.3), sin and cos are
-# within an ulp (2^-23), cos x mscale, two products and a sum round at 2^-24 each: below 2^-21 of |mscale| (|a| + |b|).
+# Rotating in fp32 (rope.cuh): the reduced angle, at most pi / 4, is rounded three times (its rest, pi / 2, their product:
+# 2.5 * 2^-24 of 0.79, below 2^-23), the series of sin and cos rounds within two halves of an ulp (2^-23), cos x mscale, two
+# products and a sum round at 2^-24 each: below 2^-21 of |mscale| (|a| + |b|).
 ROPE_ERR = 2.0 ** -21
 
 

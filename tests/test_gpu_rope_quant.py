@@ -515,6 +515,28 @@ def test_another_stream_and_captured_graph_of_a_decode_step():
         check_attention(captured[i][0], captured[i][1], captured[i][2], kk[:i + 1], vv[:i + 1], 1 / math.sqrt(d))
 
 
+def test_two_streams_at_once():
+    """Two calls in flight on two streams, each with a workspace of its own, give what they give one after the other."""
+    q, H, d, P = hsa.make_quant(1, 64), 4, 64, 3000
+    pk, pv = filled(q, 2, P, H, d, 90), filled(q, 2, P, H, d, 91)
+    Qs = [rand(9, H, d, seed=92 + i, dtype=torch.bfloat16) for i in range(2)]
+    want = [attend(q, x, pk, pv, [0, 1]) for x in Qs]
+    sel = torch.arange(2, dtype=torch.int32, device=CU)
+    streams = [torch.cuda.Stream() for _ in Qs]
+    got = []
+    torch.cuda.synchronize()
+    for s, x in zip(streams, Qs):
+        ws = workspace(hsa.hkv_attn_quant_workspace_size(9, H, H, d, 2, P))
+        out, ls = torch.empty(9, H, d, device=CU), torch.empty(9, H, device=CU)
+        s.wait_stream(torch.cuda.current_stream())
+        for _ in range(20):
+            hsa.hkv_attn_quant(q, x, pk.table, pv.table, sel, 2, P, H, out, ls, ws, stream=s)
+        got.append((out, ls, ws))
+    torch.cuda.synchronize()
+    for (o, ls, _), (a, b, ws) in zip(want, got):
+        assert torch.equal(o, a) and torch.equal(ls, b) and hsa.hsa_status_read(ws) == 0
+
+
 def test_rows_beyond_two_to_the_31_elements():
     """A page of more than 2^31 code bytes: offsets are 64-bit."""
     q, H, d = hsa.make_quant(0, 128), 40, 128

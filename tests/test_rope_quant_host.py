@@ -103,7 +103,8 @@ def test_rope_refusals(lib, fn):
         (dict(rope=rope_struct(mscale=float("nan"))), 1), (dict(rope=rope_struct(inv=None)), 1), (dict(rope=rope_struct(inv=MIS)), 1),
         (dict(rope=rope_struct(axes=(16, 16)), pos_stride=3), 1),
         (dict(qi=rows(data=None)), 1), (dict(qi=rows(data=0x10002)), 1), (dict(qi=rows(ts=132)), 1), (dict(qi=rows(hs=60)), 1),
-        (dict(qi=rows(hs=56)), 1), (dict(qi=rows(ts=-128)), 1), (dict(qo=rows(ts=0)), 1), (dict(qo=rows(H=3)), 1), (dict(qi=rows(H=0)), 1),
+        (dict(qi=rows(hs=56)), 1), (dict(qi=rows(ts=-128)), 1), (dict(qo=rows(ts=0)), 1), (dict(qo=rows(ts=64)), 1),
+        (dict(qo=rows(ts=128, hs=128)), 1), (dict(qo=rows(ts=64, hs=192)), 1), (dict(qo=rows(H=3)), 1), (dict(qi=rows(H=0)), 1),
         (dict(qi=rows(H=16385), qo=rows(H=16385)), 2),
         (dict(ki=rows()), 1), (dict(ki=rows(), ko=rows(H=1)), 1), (dict(ki=rows(), ko=rows(ts=0)), 1),
     ]
@@ -121,6 +122,7 @@ def test_rope_refusals(lib, fn):
         # fp32 strides count in 4-byte elements, a broadcast input row is allowed
         assert call_rope(lib, fn, dtype=2, qi=rows(ts=132, hs=64), qo=rows(ts=132)) == 4
         assert call_rope(lib, fn, qi=rows(ts=0)) == 4
+        assert call_rope(lib, fn, qo=rows(ts=64, hs=256)) == 4  # [H, T, d]
 
 
 def call_rows(lib, q=(0, 64), K=None, V=None, T=4, d=64, dtype=0, rope=None, pos=None, pos_stride=4, pk=P(A), pv=P(A), NP=2,
@@ -177,7 +179,7 @@ def call_attn(lib, q=(0, 64), Q=P(A), T=2, Hq=4, pk=P(A), pv=P(A), NP=4, sel=P(A
 
 def test_attn_quant_refusals(lib):
     bad = [
-        (dict(q=(0, 7)), 2), (dict(T=-1), 1), (dict(T=65), 2), (dict(Hq=3), 1), (dict(Hq=0), 1), (dict(H=0), 1), (dict(Kp=0), 1),
+        (dict(q=(0, 7)), 2), (dict(T=-1), 1), (dict(T=65), 2), (dict(Hq=3), 1), (dict(Hq=0), 1), (dict(T=64, Hq=16384, H=1), 2), (dict(Hq=16386, H=2), 2), (dict(H=0), 1), (dict(Kp=0), 1),
         (dict(Kp=5), 1), (dict(NP=0), 1), (dict(P_tok=0), 1), (dict(P_tok=2 ** 30), 2), (dict(d=80), 2), (dict(Q=None), 1),
         (dict(Q=P(MIS)), 1), (dict(out=None), 1), (dict(pk=None), 1), (dict(sel=None), 1), (dict(scale=float("nan")), 1),
         (dict(scale=-1.0), 1), (dict(scale=float("inf")), 1), (dict(ws=None), 3), (dict(wsb=255), 3), (dict(Kp=4, P_tok=4096, wsb=4096), 3),
