@@ -17,7 +17,7 @@
 //   q    bf16 has 8 significant bits; scaled per query by a power of two to magnitudes
 //        below 2 it is exact in fp16 down to 2^-24 of the query's largest element (less
 //        is rounded at 2^-25 of it);
-//   w    is split into two halves, w = hi + lo, with an error of 2^-22 of w, or 2^-25 of
+//   w    is split into two halves, w = hi + lo, with an error of 2^-22 of w, or 2^-24 of
 //        the largest weight for small ones.  To stay within fp16's range, value scales
 //        are taken relative to a running power of two per group (`vref`), which only rises;
 //        the accumulators are rescaled when it does, as when the running maximum rises.
@@ -52,7 +52,7 @@ constexpr int kAqMostCtas = 4;
 // CTAs on an SM, with up to 8 (NT = 1) or 16 queries to a tile: as many as registers and the ring allow.
 template <int FMT, int D, int GROUP, int NT>
 constexpr int ctas_per_sm() {
-  if (NT == 2) return 2;
+  if (NT == 2) return D == 64 ? 3 : 2;
   if (D == 64) return 4;
   return code_bits<FMT>() == 8 && GROUP == 32 ? 2 : 3;
 }
@@ -166,6 +166,13 @@ __device__ __forceinline__ void two_keys(const uint32_t* a, const uint32_t* b, i
       p1 = hsub2_u(__byte_perm(x, 0x64646464u, 0x4342), 0x64806480u);
     }
   }
+}
+
+// 2^x within 2 ulp; results below 2^-126 are zero.
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 __device__ __forceinline__ float pow2_below(float x) {  // the power of two at or below x, within [2^-126, 2^126]
@@ -341,15 +348,17 @@ __global__ void __launch_bounds__(kAqThreads, (ctas_per_sm<FMT, D, GROUP, NT>())
   }
 
   float o[NT][G * KS][4];
-  // the reference that scores are taken relative to, and the value scales of each group: raised
-  // when something in a tile is more than 2^6 above them, so that weights stay below 2^12
-  float m[NT][2], ref[NT][2], l[NT][2], vref[G];
+  // the references that products are taken relative to (before qs, so that the largest differs
+  // from itself by nothing) and the value scales of each group: raised when something in a tile is
+  // more than 2^6 above them, so that weights stay below 2^12
+  float m[NT][2], ref[NT][2], high_at[NT][2], l[NT][2], vref[G];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
 #pragma unroll
     for (int k = 0; k < G * KS; ++k) o[n][k][0] = o[n][k][1] = o[n][k][2] = o[n][k][3] = 0.f;
     m[n][0] = m[n][1] = -INFINITY;
     ref[n][0] = ref[n][1] = 0.f;  // m, or 0 while that is -inf
+    high_at[n][0] = high_at[n][1] = -INFINITY;  // m + 6 / qs: what a product has to be above
     l[n][0] = l[n][1] = 0.f;
   }
 #pragma unroll
@@ -395,19 +404,29 @@ __global__ void __launch_bounds__(kAqThreads, (ctas_per_sm<FMT, D, GROUP, NT>())
         }
       }
     }
+    if (valid < kAqRows) {
+#pragma unroll
+      for (int mi = 0; mi < M; ++mi)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (16 * mi + g + 8 * (e >> 1) >= valid) s[mi][n][e] = -INFINITY;
+    }
     // value scales of keys g and g + 8, and whether a reference has to be raised
     float vs[M][2][G];
     bool high = false;
 #pragma unroll
-    for (int mi = 0; mi < M; ++mi) {
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int e = 0; e < 2; ++e) {
+        float top = fmaxf(s[0][n][e], s[0][n][2 + e]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float x = s[mi][n][e] * qs[n][e & 1];
-          s[mi][n][e] = 16 * mi + g + 8 * (e >> 1) < valid ? x : -INFINITY;
-          high |= s[mi][n][e] > m[n][e & 1] + 6.f;
-        }
+        for (int mi = 1; mi < M; ++mi) top = fmaxf(top, fmaxf(s[mi][n][e], s[mi][n][2 + e]));
+        high |= top > high_at[n][e];
+      }
+#pragma unroll
+    for (int mi = 0; mi < M; ++mi)
 #pragma unroll
       for (int r = 0; r < 2; ++r)
 #pragma unroll
@@ -415,7 +434,6 @@ __global__ void __launch_bounds__(kAqThreads, (ctas_per_sm<FMT, D, GROUP, NT>())
           vs[mi][r][k] = v_scale[(16 * mi + g + 8 * r) * SF + k];
           high |= fabsf(vs[mi][r][k]) > 64.f * vref[k];
         }
-    }
     if (__any_sync(0xffffffffu, high)) {
       float alpha[NT][2];
 #pragma unroll
@@ -429,8 +447,9 @@ __global__ void __launch_bounds__(kAqThreads, (ctas_per_sm<FMT, D, GROUP, NT>())
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
           ref[n][e] = top == -INFINITY ? 0.f : top;
-          alpha[n][e] = exp2f(m[n][e] - ref[n][e]);
+          alpha[n][e] = exp2f((m[n][e] - ref[n][e]) * qs[n][e]);
           m[n][e] = top;
+          high_at[n][e] = top + 6.f / qs[n][e];
           l[n][e] *= alpha[n][e];
         }
 #pragma unroll
@@ -458,7 +477,7 @@ __global__ void __launch_bounds__(kAqThreads, (ctas_per_sm<FMT, D, GROUP, NT>())
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          s[mi][n][e] = exp2f(s[mi][n][e] - ref[n][e & 1]);
+          s[mi][n][e] = exp2_approx((s[mi][n][e] - ref[n][e & 1]) * qs[n][e & 1]);
           l[n][e & 1] += s[mi][n][e];
         }
       // O += V w, group by group; values 2t, 2t + 1, 2t + 8, 2t + 9
@@ -477,10 +496,11 @@ __global__ void __launch_bounds__(kAqThreads, (ctas_per_sm<FMT, D, GROUP, NT>())
           for (int r = 0; r < 2; ++r) {
             const float scale = vs[mi][r][k] * inv;
             const float w0 = s[mi][n][2 * r] * scale, w1 = s[mi][n][2 * r + 1] * scale;
-            const uint32_t hh = pack_half2(w0, w1);
-            const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hh));
-            hi[n][r] = movmatrix(hh);
-            lo[n][r] = movmatrix(pack_half2(w0 - back.x, w1 - back.y));
+            // the upper 11 bits, which a half holds, and the rest
+            const float h0 = __uint_as_float(__float_as_uint(w0) & 0xffffe000u);
+            const float h1 = __uint_as_float(__float_as_uint(w1) & 0xffffe000u);
+            hi[n][r] = movmatrix(pack_half2(h0, h1));
+            lo[n][r] = movmatrix(pack_half2(w0 - h0, w1 - h1));
           }
 #pragma unroll
         for (int mt = 0; mt < KS; ++mt) {
@@ -507,6 +527,7 @@ __global__ void __launch_bounds__(kAqThreads, (ctas_per_sm<FMT, D, GROUP, NT>())
       sum += __shfl_xor_sync(0xffffffffu, sum, 4);
       sum += __shfl_xor_sync(0xffffffffu, sum, 8);
       sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+      m[n][e] = m[n][e] == -INFINITY ? -INFINITY : m[n][e] * qs[n][e];  // in log2 units from here on
       if (g == 0) {
         s_m[warp][n * 8 + 2 * t + e] = m[n][e];
         s_l[warp][n * 8 + 2 * t + e] = sum;
