@@ -243,6 +243,12 @@ __global__ void __launch_bounds__(kAqThreads, (ctas_per_sm<FMT, D, GROUP, NT>())
   constexpr int PER = TILE / ROWS_AT_ONCE;
   const int my_row = tid / CH, my_vec = tid % CH;
   const int my_head = my_vec / (CH / HEADS), my_col = my_vec % (CH / HEADS) * 16;
+  // where a row's vector goes in a tile: my_row's place, and from there each ROWS_AT_ONCE-th row's
+  const int my_place = (my_row / kAqRows * HEADS + my_head) * St::kUnit + my_row % kAqRows * St::kPitch + my_col;
+  auto place_of = [](int i) {
+    return i * ROWS_AT_ONCE / kAqRows * HEADS * St::kUnit + i * ROWS_AT_ONCE % kAqRows * St::kPitch;
+  };
+  static_assert(kAqRows % ROWS_AT_ONCE == 0 || ROWS_AT_ONCE % kAqRows == 0, "rows keep their unit");
   constexpr int SF = HEADS * G;                      // scales of a row
   const long long row_step = (long long)a.q.H * St::kRow, scale_step = (long long)a.q.H * 4 * G;
   const bool wide = SF % 4 == 0 && scale_step % 16 == 0;  // scales in 16-byte vectors (else one by one)
@@ -268,18 +274,26 @@ __global__ void __launch_bounds__(kAqThreads, (ctas_per_sm<FMT, D, GROUP, NT>())
       if (kbase) {
         const int row0 = in_page * TILE;
         valid = min((slot < whole ? P : rest) - row0, TILE);
-        const uint32_t dst = ring_s + stage * St::kBytes;
+        const uint32_t dst = ring_s + stage * St::kBytes, to = dst + my_place;
         const long long from = (row0 + my_row) * row_step + h0 * St::kRow + my_vec * 16;
         const char *k = kbase + from, *v = vbase + from;
+        if (valid == TILE) {
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-          const int row = my_row + i * ROWS_AT_ONCE;
-          const uint32_t to = dst + (row / kAqRows * HEADS + my_head) * St::kUnit + row % kAqRows * St::kPitch + my_col;
-          const bool on = row < valid;  // zeros behind the last row
-          cp_async_zero<16>(to, on ? k : kbase, on);
-          cp_async_zero<16>(to + St::kV, on ? v : vbase, on);
-          k += ROWS_AT_ONCE * row_step;
-          v += ROWS_AT_ONCE * row_step;
+          for (int i = 0; i < PER; ++i) {
+            cp_async<16>(to + place_of(i), k);
+            cp_async<16>(to + place_of(i) + St::kV, v);
+            k += ROWS_AT_ONCE * row_step;
+            v += ROWS_AT_ONCE * row_step;
+          }
+        } else {  // zeros behind the last row
+#pragma unroll
+          for (int i = 0; i < PER; ++i) {
+            const bool on = my_row + i * ROWS_AT_ONCE < valid;
+            cp_async_zero<16>(to + place_of(i), on ? k : kbase, on);
+            cp_async_zero<16>(to + place_of(i) + St::kV, on ? v : vbase, on);
+            k += ROWS_AT_ONCE * row_step;
+            v += ROWS_AT_ONCE * row_step;
+          }
         }
         for (int i = tid; i < TILE * pieces; i += kAqThreads) {
           const int row = i / pieces, at = i - row * pieces;

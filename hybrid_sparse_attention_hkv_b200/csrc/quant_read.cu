@@ -4,8 +4,9 @@
 // HBM bound, two thirds and more of it writes: 1 or 1/2 byte read and 2 written an element.
 // What counts beside enough loads in flight is that the CTAs which run at one time write
 // neighbouring memory: 16-row CTAs (a window of some 70 MB, all of it written from end to
-// end) reach 95% of the copy rate without a rotation, where CTAs of 128 rows, each on a
-// stretch of its own, stay at 85%.
+// end) reach 99% of the copy rate without a rotation, where CTAs of 128 rows, each on a
+// stretch of its own, stayed at 85%.  After that it is the instructions: with addresses that
+// are a pointer and a constant, a rotated cache with its means takes 250 us instead of 272.
 #include "common.cuh"
 #include "kernels.h"
 #include "quant.cuh"
@@ -48,8 +49,8 @@ struct ReadArgs {
   int* status;
 };
 
-// A thread's way through its rows phase, phase + phases, ... of a CTA: where the next one's
-// codes and scales are.
+// A thread's way through its rows phase, phase + phases, ... of a CTA: where the codes of its
+// chunk `lo` of the next one are, and their scale.
 template <int FMT, int J>
 struct ReadCursor {
   const char* codes;
@@ -57,11 +58,11 @@ struct ReadCursor {
   long long code_step, scale_step;
   int row;         // next row
   int left;        // rows from there to its page's end
-  int slot, phases;
+  int phases;
 
-  __device__ __forceinline__ void seek(const ReadArgs& a, const void* const* table, int r0, int h) {
+  __device__ __forceinline__ void seek(const ReadArgs& a, const void* const* table, int r0, int h, const ChunkPair& c) {
     constexpr int D = 16 * J;
-    slot = (unsigned)(r0 + row) / (unsigned)a.q.P_tok;
+    const int slot = (unsigned)(r0 + row) / (unsigned)a.q.P_tok;
     const int t = r0 + row - slot * a.q.P_tok;
     left = a.q.P_tok - t;
     const int p = a.sel[slot];
@@ -71,12 +72,13 @@ struct ReadCursor {
       set_status(a.status, HSA_ERR_DEVICE);
     } else {
       const long long head_row = (long long)t * a.q.H + h;
-      codes = base + head_row * (D * code_bits<FMT>() / 8);
-      scales = reinterpret_cast<const float*>(base + a.q.scale_offset) + head_row * (D / a.q.group);
+      codes = base + head_row * (D * code_bits<FMT>() / 8) + c.lo * code_bits<FMT>();
+      scales = reinterpret_cast<const float*>(base + a.q.scale_offset) + head_row * (D / a.q.group) + c.lo * 8 / a.q.group;
     }
   }
   // The step to the next row; false at the CTA's end.
-  __device__ __forceinline__ bool next(const ReadArgs& a, const void* const* table, int r0, int h, int rows) {
+  __device__ __forceinline__ bool next(const ReadArgs& a, const void* const* table, int r0, int h, const ChunkPair& c,
+                                       int rows) {
     row += phases;
     if (row >= rows) return false;
     left -= phases;
@@ -86,7 +88,7 @@ struct ReadCursor {
         scales += scale_step;
       }
     } else {
-      seek(a, table, r0, h);
+      seek(a, table, r0, h, c);
     }
     return true;
   }
@@ -97,8 +99,10 @@ struct ReadCursor {
 // again one round after it was read.
 template <int FMT>
 struct ReadSlot {
-  static constexpr int kCodeBytes = code_bits<FMT>();  // of 8 columns
-  static constexpr int kBytes = 2 * kCodeBytes + 8;    // lo and hi chunk, their two scales
+  static constexpr int kCodeBytes = code_bits<FMT>();               // of 8 columns
+  static constexpr int kHi = kReadThreads * kCodeBytes;             // lo chunks of all threads, their hi chunks,
+  static constexpr int kScales = 2 * kHi;                           // ... the two scales
+  static constexpr int kBytes = kScales + 8 * kReadThreads;
 };
 
 template <int FMT, int J, int ROPE, bool POOL>
@@ -115,7 +119,8 @@ __device__ __forceinline__ void read_rows(const ReadArgs& a, const ReadArgs::Par
   const int j = item % J, h = h0 + item / J;
   const bool active = phase < phases && item < items;
   const ChunkPair c = chunk_pair<J, ROPE>(a.r, j);
-  const int lo_group = c.lo * 8 / q.group, hi_group = c.hi * 8 / q.group;
+  const int next_group = c.hi * 8 / q.group - c.lo * 8 / q.group;  // from lo's scale to hi's
+  const int next_chunk = (ROPE == kRopeHalf ? c.hi - c.lo : J) * BITS;
   float acc[16];
 #pragma unroll
   for (int k = 0; k < 16; ++k) acc[k] = 0.f;
@@ -125,61 +130,62 @@ __device__ __forceinline__ void read_rows(const ReadArgs& a, const ReadArgs::Par
   at.scale_step = (long long)phases * q.H * (D / q.group);
   at.row = phase;
   bool more = active && phase < rows;
-  if (more) at.seek(a, table, r0, h);
-  // the ring lies behind the cos and sin: lo codes, hi codes, scales, each [slot][thread]
-  constexpr int CB = ReadSlot<FMT>::kCodeBytes;
+  if (more) at.seek(a, table, r0, h, c);
+  // the ring lies behind the cos and sin
+  using Slot = ReadSlot<FMT>;
+  constexpr int CB = Slot::kCodeBytes;
   const int threads = blockDim.x;
-  char* ring = reinterpret_cast<char*>(smem) + a.ring_offset;
-  char* ring_lo = ring + tid * CB;
-  char* ring_hi = ring_lo + kReadRing * threads * CB;
-  char* ring_s = ring + 2 * kReadRing * threads * CB + tid * 8;
-  const uint32_t dst_lo = smem_u32(ring_lo), dst_hi = smem_u32(ring_hi), dst_s = smem_u32(ring_s);
-  uint32_t there = 0;  // bit s: slot s holds a row
-  auto ask = [&](int slot) {
-    there &= ~(1u << slot);
+  char* codes = reinterpret_cast<char*>(smem) + a.ring_offset + tid * CB;
+  char* scales = reinterpret_cast<char*>(smem) + a.ring_offset + Slot::kScales + tid * 8;
+  const uint32_t to_codes = smem_u32(codes), to_scales = smem_u32(scales);
+  uint32_t there = 0;  // whether the rows asked for are, the last one in bit 0
+  auto ask = [&](int slot) {  // slot: its offset in the ring
+    there <<= 1;
     if (more) {
       if (at.codes) {
-        there |= 1u << slot;
-        cp_async<CB>(dst_lo + slot * threads * CB, at.codes + c.lo * BITS);
-        cp_async<CB>(dst_hi + slot * threads * CB, at.codes + c.hi * BITS);
-        cp_async<4>(dst_s + slot * threads * 8, at.scales + lo_group);
-        cp_async<4>(dst_s + slot * threads * 8 + 4, at.scales + hi_group);
+        there |= 1u;
+        cp_async<CB>(to_codes + slot, at.codes);
+        cp_async<CB>(to_codes + slot + Slot::kHi, at.codes + next_chunk);
+        cp_async<4>(to_scales + slot, at.scales);
+        if (next_group != 0) cp_async<4>(to_scales + slot + 4, at.scales + next_group);
       }
-      more = at.next(a, table, r0, h, rows);
+      more = at.next(a, table, r0, h, c, rows);
     }
     cp_async_commit();
   };
 #pragma unroll
-  for (int s = 0; s < kReadRing - 1; ++s) ask(s);
-  uint16_t* out = dst + ((long long)(r0 + phase) * q.H + h) * D;
+  for (int s = 0; s < kReadRing - 1; ++s) ask(s * Slot::kBytes);
+  uint16_t* out = dst + ((long long)(r0 + phase) * q.H + h) * D + c.lo * 8;
   const long long out_step = (long long)phases * q.H * D;
-  int slot = 0, i = phase;
+  const int out_hi = next_chunk / BITS * 8;
+  int slot = 0, last = (kReadRing - 1) * Slot::kBytes, i = phase;
   for (int b0 = 0; b0 < rows; b0 += kReadBatch) {
     if constexpr (ROPE != kRopeNone) {
       if (b0) __syncthreads();  // the last rows' cos and sin have been read
       rope_table<J, ROPE>(a.r, r0 + b0, min(kReadBatch, rows - b0), reinterpret_cast<float4*>(smem), tid, threads);
       __syncthreads();
     }
+    const float4* turn = reinterpret_cast<const float4*>(smem) + (i - b0) * 4 * J;
     const int end = active ? min(rows, b0 + kReadBatch) : 0;
     for (; i < end; i += phases) {
-      ask(slot == 0 ? kReadRing - 1 : slot - 1);
+      ask(last);
       cp_async_wait<kReadRing - 1>();
-      if (there >> slot & 1) {
+      if (there >> (kReadRing - 1) & 1) {
         Codes8<FMT> lo, hi;
         if constexpr (FMT == HKV_QUANT_INT4) {
-          lo.w[0] = *reinterpret_cast<const uint32_t*>(ring_lo + slot * threads * CB);
-          hi.w[0] = *reinterpret_cast<const uint32_t*>(ring_hi + slot * threads * CB);
+          lo.w[0] = *reinterpret_cast<const uint32_t*>(codes + slot);
+          hi.w[0] = *reinterpret_cast<const uint32_t*>(codes + slot + Slot::kHi);
         } else {
-          const uint2 u = *reinterpret_cast<const uint2*>(ring_lo + slot * threads * CB);
-          const uint2 v = *reinterpret_cast<const uint2*>(ring_hi + slot * threads * CB);
+          const uint2 u = *reinterpret_cast<const uint2*>(codes + slot);
+          const uint2 v = *reinterpret_cast<const uint2*>(codes + slot + Slot::kHi);
           lo.w[0] = u.x; lo.w[1] = u.y;
           hi.w[0] = v.x; hi.w[1] = v.y;
         }
-        const float2 s = *reinterpret_cast<const float2*>(ring_s + slot * threads * 8);
+        const float2 s = *reinterpret_cast<const float2*>(scales + slot);
         float x[8], y[8];
         decode8<FMT>(lo, s.x, x);
-        decode8<FMT>(hi, s.y, y);
-        rotate_chunks<J, ROPE>(c, reinterpret_cast<const float4*>(smem) + (i - b0) * 4 * J, j, x, y);
+        decode8<FMT>(hi, next_group != 0 ? s.y : s.x, y);
+        rotate_chunks<J, ROPE>(c, turn, j, x, y);
         if constexpr (POOL) {
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
@@ -189,12 +195,14 @@ __device__ __forceinline__ void read_rows(const ReadArgs& a, const ReadArgs::Par
         }
         Chunk<__nv_bfloat16> w;
         w.set(x);
-        w.store(out + c.lo * 8);
+        w.store(out);
         w.set(y);
-        w.store(out + c.hi * 8);
+        w.store(out + out_hi);
       }
       out += out_step;
-      slot = slot == kReadRing - 1 ? 0 : slot + 1;
+      turn += phases * 4 * J;
+      last = slot;
+      slot = slot == (kReadRing - 1) * Slot::kBytes ? 0 : slot + Slot::kBytes;
     }
   }
   cp_async_wait<0>();
@@ -216,7 +224,7 @@ __device__ __forceinline__ void read_rows(const ReadArgs& a, const ReadArgs::Par
 }
 
 // (Both members of eight pairs and their sums at once are too much for 64 registers: with two
-// CTAs an SM and no spills the half layout's block means take 276 us where three take 300.)
+// CTAs an SM and no spills the half layout's block means take 265 us where three took 300.)
 template <int FMT, int J, int ROPE, bool POOL>
 __global__ void __launch_bounds__(kReadThreads, ROPE == kRopeHalf && POOL ? 2 : kReadCtas) gather_quant_kernel(const ReadArgs a) {
   extern __shared__ __align__(16) float smem[];
@@ -257,7 +265,7 @@ cudaError_t launch_read(ReadArgs& a, cudaStream_t s) {
   const size_t pool = POOL ? (size_t)threads * 16 * sizeof(float) : 0;
   if (pool > smem) smem = pool;
   a.ring_offset = (int)smem;
-  smem += (size_t)kReadRing * threads * ReadSlot<FMT>::kBytes;
+  smem += (size_t)kReadRing * ReadSlot<FMT>::kBytes;
   if (smem > kDefaultSmemOptIn) {
     const cudaError_t e = cudaFuncSetAttribute(gather_quant_kernel<FMT, J, ROPE, POOL>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
