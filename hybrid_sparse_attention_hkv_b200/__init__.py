@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from contextlib import contextmanager
 from dataclasses import dataclass
 
@@ -72,11 +73,6 @@ class _Rope(ctypes.Structure):
                 ("axis_pairs", ctypes.c_int * 3), ("mscale", ctypes.c_float), ("inv_freq", ctypes.c_void_p)]
 
 
-class _Rows(ctypes.Structure):
-    _fields_ = [("data", ctypes.c_void_p), ("H", ctypes.c_int), ("token_stride", ctypes.c_longlong),
-                ("head_stride", ctypes.c_longlong)]
-
-
 class Quant(ctypes.Structure):
     """hkv_quant_t: the format of quantised pages and the columns a scale covers."""
     _fields_ = [("format", ctypes.c_int), ("group", ctypes.c_int)]
@@ -95,7 +91,7 @@ def load_library(path: str = LIB_PATH):
     lib = ctypes.CDLL(path)
     P, I, L, S, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_size_t, ctypes.c_float
     CP = ctypes.POINTER(Config)
-    RP, XP, QP = ctypes.POINTER(_Rope), ctypes.POINTER(_Rows), ctypes.POINTER(Quant)
+    RP, XP, QP = ctypes.POINTER(_Rope), P, ctypes.POINTER(Quant)  # XP: a packed hsa_rows_t
     sig = {
         "hsa_status_string": (ctypes.c_char_p, [I]),
         "hsa_last_error_detail": (ctypes.c_char_p, []),
@@ -455,12 +451,21 @@ def _refuse(where, detail):
     raise HsaError(1, where, detail)
 
 
+# These checks are most of a short call's time, so they are written for the case that passes: devices as indices (-1: the
+# CPU), hsa_rows_t packed in one go.
+_pack_rows = struct.Struct("@Piqq").pack
+
+
+def _not_fitting(t, what, where, device, dtype):
+    if t.get_device() != device:
+        _refuse(where, f"{what} is on {t.device}, not on " + ("the CPU" if device < 0 else f"cuda:{device}"))
+    _refuse(where, f"{what} is {t.dtype}, not {dtype}")
+
+
 def _tensor(t, what, where, device, dtype, shape=None):
-    """A dense device tensor of `dtype` (and `shape`): its address."""
-    if t.device != device:
-        _refuse(where, f"{what} is on {t.device}, not on {device}")
-    if t.dtype != dtype:
-        _refuse(where, f"{what} is {t.dtype}, not {dtype}")
+    """A dense tensor of `dtype` (and `shape`) on device `device`: its address."""
+    if t.dtype is not dtype or t.get_device() != device:
+        _not_fitting(t, what, where, device, dtype)
     if shape is not None and t.shape != shape:
         _refuse(where, f"{what} is {list(t.shape)}, not {list(shape)}")
     if not t.is_contiguous():
@@ -470,34 +475,33 @@ def _tensor(t, what, where, device, dtype, shape=None):
 
 def _rows(t, what, where, device, dtype, T, d):
     """Token rows [T, H, d] whose columns are dense, as an hsa_rows_t."""
-    if t.device != device:
-        _refuse(where, f"{what} is on {t.device}, not on {device}")
-    if t.dtype != dtype:
-        _refuse(where, f"{what} is {t.dtype}, not {dtype}")
+    if t.dtype is not dtype or t.get_device() != device:
+        _not_fitting(t, what, where, device, dtype)
     shape = t.shape
     if len(shape) != 3 or shape[0] != T or shape[2] != d:
         _refuse(where, f"{what} is {list(shape)}, not [{T}, heads, {d}]")
     step, head, column = t.stride()
     if column != 1:
         _refuse(where, f"the columns of {what} are not contiguous (stride {column})")
-    if shape[1] == 1:  # torch gives a dimension of one element any stride
+    H = shape[1]
+    if H == 1:  # torch gives a dimension of one element any stride
         head = d
     if T == 1:
-        step = shape[1] * head
-    return _Rows(t.data_ptr(), shape[1], step, head)
+        step = H * head
+    return _pack_rows(t.data_ptr(), H, step, head)
 
 
 def _launch(where, device, stream, fn, *args):
-    """fn(*args, stream) with `device` current: on `stream`, or on the device's current one."""
-    if device.type != "cuda":
-        _refuse(where, f"the tensors are on {device}, not on a CUDA device")
+    """fn(*args, stream) with device `device` current: on `stream`, or on the device's current one."""
+    if device < 0:
+        _refuse(where, "the tensors are on the CPU, not on a CUDA device")
     if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(device.index)  # torch.cuda.current_stream takes 3 us more
-    elif stream.device != device:
-        _refuse(where, f"the stream is on {stream.device}, not on {device}")
+        raw = torch._C._cuda_getCurrentRawStream(device)  # torch.cuda.current_stream takes 3 us more
+    elif stream.device.index != device:
+        _refuse(where, f"the stream is on {stream.device}, not on cuda:{device}")
     else:
         raw = stream.cuda_stream
-    if device.index == torch.cuda.current_device():
+    if device == torch.cuda.current_device():
         code = fn(*args, raw)
     else:
         with torch.cuda.device(device):
@@ -510,8 +514,9 @@ class Rope:
     """hsa_rope_t with the table it points at (make_rope)."""
 
     def __init__(self, inv_freq, layout, axis_pairs, mscale):
-        self.inv_freq, self.device, self.n_axes = inv_freq, inv_freq.device, len(axis_pairs)
+        self.inv_freq, self.device, self.n_axes = inv_freq, inv_freq.get_device(), len(axis_pairs)
         self.c = _Rope(layout, 2 * inv_freq.numel(), self.n_axes, (ctypes.c_int * 3)(*axis_pairs), mscale, inv_freq.data_ptr())
+        self.ref = ctypes.byref(self.c)
 
 
 def rope_freqs(dim, base=10000.0, scaling=ROPE_SCALE_NONE, factor=1.0, orig_context=0):
@@ -529,7 +534,7 @@ def make_rope(inv_freq, layout=ROPE_INTERLEAVED, axis_pairs=None, mscale=1.0) ->
     pairs = [inv_freq.numel()] if axis_pairs is None else [int(n) for n in axis_pairs]
     if inv_freq.dim() != 1 or not 1 <= len(pairs) <= 3 or sum(pairs) != inv_freq.numel() or min(pairs) < 0:
         _refuse("make_rope", f"inv_freq {list(inv_freq.shape)} for the axes' pairs {pairs}")
-    _tensor(inv_freq, "inv_freq", "make_rope", inv_freq.device, torch.float64)
+    _tensor(inv_freq, "inv_freq", "make_rope", inv_freq.get_device(), torch.float64)
     return Rope(inv_freq, layout, pairs, mscale)
 
 
@@ -542,28 +547,27 @@ def _positions(rope, pos, where, device, tokens):
     if pos is None:
         _refuse(where, "rope without pos")
     if rope.device != device:
-        _refuse(where, f"inv_freq is on {rope.device}, not on {device}")
+        _refuse(where, f"inv_freq is on {rope.inv_freq.device}, not on " + ("the CPU" if device < 0 else f"cuda:{device}"))
     want = (rope.n_axes, tokens)
     if pos.shape != want and (rope.n_axes != 1 or pos.shape != (tokens,)):
         _refuse(where, f"pos is {list(pos.shape)}, not {list(want)}")
-    return ctypes.byref(rope.c), _tensor(pos, "pos", where, device, torch.int32), tokens
+    return rope.ref, _tensor(pos, "pos", where, device, torch.int32), tokens
 
 
 def _rope_call(name, rope, pos, q, q_out, k, k_out, stream):
-    device, dtype = q.device, q.dtype
-    if q.dim() != 3 or dtype not in _DTYPES:
-        _refuse(name, f"q is {list(q.shape)} {dtype}: [T, heads, d] bfloat16, float16 or float32 wanted")
-    T, _, d = q.shape
+    device, dtype, shape = q.get_device(), q.dtype, q.shape
+    if len(shape) != 3 or dtype not in _DTYPES:
+        _refuse(name, f"q is {list(shape)} {dtype}: [T, heads, d] bfloat16, float16 or float32 wanted")
+    T, _, d = shape
     qi, qo = _rows(q, "q", name, device, dtype, T, d), _rows(q_out, "q_out", name, device, dtype, T, d)
     ki = ko = None
     if (k is None) != (k_out is None):
         _refuse(name, "k and k_out go together")
     if k is not None:
-        ki = ctypes.byref(_rows(k, "k", name, device, dtype, T, d))
-        ko = ctypes.byref(_rows(k_out, "k_out", name, device, dtype, T, d))
+        ki = _rows(k, "k", name, device, dtype, T, d)
+        ko = _rows(k_out, "k_out", name, device, dtype, T, d)
     r, at, step = _positions(rope, pos, name, device, T)
-    _launch(name, device, stream, getattr(load_library(), name), r, at, step, T, d, _DTYPES[dtype], ctypes.byref(qi),
-            ctypes.byref(qo), ki, ko)
+    _launch(name, device, stream, getattr(load_library(), name), r, at, step, T, d, _DTYPES[dtype], qi, qo, ki, ko)
 
 
 def hsa_rope(rope, pos, q, q_out, k=None, k_out=None, stream=None):
@@ -600,7 +604,7 @@ def hkv_quant_rows(quant: Quant, K, V, page_k_ptrs, page_v_ptrs, P_tok, first_ro
                    pos=None, stream=None):
     """Quantise rows K, V [T, H, d] (bfloat16, float16 or float32, strided as hsa_rope's) into history rows
     first_row (+ first_row_dev, a device int64 scalar), ... of the pages; `rope` rotates the keys first."""
-    where, device, dtype = "hkv_quant_rows", K.device, K.dtype
+    where, device, dtype = "hkv_quant_rows", K.get_device(), K.dtype
     if K.dim() != 3 or dtype not in _DTYPES:
         _refuse(where, f"K is {list(K.shape)} {dtype}: [T, heads, d] bfloat16, float16 or float32 wanted")
     T, _, d = K.shape
@@ -610,14 +614,14 @@ def hkv_quant_rows(quant: Quant, K, V, page_k_ptrs, page_v_ptrs, P_tok, first_ro
     dev = None
     if first_row_dev is not None:
         dev = _tensor(first_row_dev.view(-1), "first_row_dev", where, device, torch.int64, (1,))
-    _launch(where, device, stream, load_library().hkv_quant_rows, ctypes.byref(quant), ctypes.byref(k), ctypes.byref(v), T, d,
-            _DTYPES[dtype], r, at, step, pk, pv, NP, P_tok, first_row, dev, w, wn)
+    _launch(where, device, stream, load_library().hkv_quant_rows, ctypes.byref(quant), k, v, T, d, _DTYPES[dtype], r, at, step,
+            pk, pv, NP, P_tok, first_row, dev, w, wn)
 
 
 def hkv_gather_quant(quant: Quant, page_k_ptrs, page_v_ptrs, sel, Kp, P_tok, H, d, Kc, Vc, ws, kbar128=None, rope=None,
                      pos=None, stream=None):
     """hkv_gather from quantised pages; `rope` rotates active-cache row r by pos[:, r] (int32 [n_axes, Kp * P_tok])."""
-    where, device = "hkv_gather_quant", Kc.device
+    where, device = "hkv_gather_quant", Kc.get_device()
     pk, pv, NP, w, wn = _tables(where, device, page_k_ptrs, page_v_ptrs, ws)
     Lc = Kp * P_tok
     s = _tensor(sel, "sel", where, device, torch.int32, (Kp,))
@@ -640,7 +644,7 @@ def hkv_attn_quant(quant: Quant, Q, page_k_ptrs, page_v_ptrs, sel, Kp, P_tok, H,
                    stream=None):
     """Attention of a few queries Q [T, Hq, d] over the first n_rows (device int32 scalar; None: all) rows of the
     selected pages of H heads.  out: [T, Hq, d] float32 or bfloat16; lse: [T, Hq] float32 or None."""
-    where, device = "hkv_attn_quant", Q.device
+    where, device = "hkv_attn_quant", Q.get_device()
     if Q.dim() != 3 or out.dtype not in (torch.float32, torch.bfloat16):
         _refuse(where, f"Q is {list(Q.shape)}, out {out.dtype}: [T, heads, d], and float32 or bfloat16, wanted")
     T, Hq, d = Q.shape

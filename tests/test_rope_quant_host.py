@@ -80,9 +80,20 @@ def rope_struct(**kw):
     return hsa._Rope(v["layout"], v["rot"], len(v["axes"]), (ctypes.c_int * 3)(*v["axes"]), v["mscale"], v["inv"])
 
 
+class Rows(ctypes.Structure):  # hsa_rows_t
+    _fields_ = [("data", ctypes.c_void_p), ("H", ctypes.c_int), ("token_stride", ctypes.c_longlong),
+                ("head_stride", ctypes.c_longlong)]
+
+
 def rows(**kw):
     v = dict(data=A, H=2, ts=128, hs=64) | kw
-    return hsa._Rows(v["data"], v["H"], v["ts"], v["hs"])
+    return Rows(v["data"], v["H"], v["ts"], v["hs"])
+
+
+def test_the_binding_packs_rows_as_the_structure():
+    t = torch.zeros(5, 4, 64, dtype=torch.float16)[:, 1:3]
+    assert hsa._rows(t, "t", "here", -1, torch.float16, 5, 64) == bytes(Rows(t.data_ptr(), 2, 256, 64))
+    assert hsa._rows(t[:1, :1], "t", "here", -1, torch.float16, 1, 64) == bytes(Rows(t.data_ptr(), 1, 64, 64))
 
 
 def call_rope(lib, fn="hsa_rope", rope=None, pos=A, pos_stride=4, T=4, d=64, dtype=0, qi=None, qo=None, ki=None, ko=None):
