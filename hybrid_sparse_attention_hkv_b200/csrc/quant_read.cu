@@ -262,8 +262,7 @@ cudaError_t launch_read(ReadArgs& a, cudaStream_t s) {
   const int need = max(a.k.slab * a.k.phases, a.v.slab * a.v.phases) * J;
   const int threads = max(8 * J, (need + 31) / 32 * 32);  // 8 J: the cos and sin of a row
   size_t smem = ROPE != kRopeNone ? (size_t)kReadBatch * 8 * J * sizeof(float2) : 0;
-  const size_t pool = POOL ? (size_t)threads * 16 * sizeof(float) : 0;
-  if (pool > smem) smem = pool;
+  if (POOL) smem = max(smem, (size_t)threads * 16 * sizeof(float));
   a.ring_offset = (int)smem;
   smem += (size_t)kReadRing * ReadSlot<FMT>::kBytes;
   if (smem > kDefaultSmemOptIn) {

@@ -3,7 +3,8 @@
 //
 // HBM bound: an element is read (2 or 4 bytes) and its code written (1 or 1/2), both once.
 // Threads share a head as in rope.cuh: d / 16 of them, two 8-column chunks each, so that a
-// group's largest magnitude is a few warp shuffles and a rotation needs none.
+// group's largest magnitude is a few warp shuffles and a rotation needs none.  12480 rows of 40
+// heads, bf16 to e4m3 with the keys rotated, 387 MB, take 60 us (0.98 of the copy rate).
 #include "common.cuh"
 #include "kernels.h"
 #include "quant.cuh"
@@ -13,9 +14,10 @@ namespace hsa {
 namespace {
 
 // A CTA takes a few tokens' K or V and a slab of heads: thread (head, j, phase) owns two
-// chunks of the tokens phase, phase + phases, ...  It asks for its first elements, then the
-// CTA computes the tokens' places and their cos and sin into shared memory while those are
-// on the way; after that a round's elements are asked for during the round before.
+// chunks of the tokens phase, phase + phases, ...  Its elements of the next two rounds are
+// always on their way to a ring in shared memory that it alone reads (74 us with one round
+// ahead in registers, 97 with K and V of a head in one thread and nothing ahead); the tokens'
+// places and their cos and sin are computed while the first ones are.
 constexpr int kRowsThreads = 320;
 constexpr int kRowsCtas = 4;   // on an SM
 constexpr int kRowsRing = 3;

@@ -3,7 +3,10 @@
 //
 // HBM bound: 2 x size bytes and 3 FLOP an element.  A CTA takes a few tokens with all their
 // heads (queries, then keys).  Its threads first ask for their elements, then compute the
-// tokens' cos and sin into shared memory while those are on the way.
+// tokens' cos and sin into shared memory while those are on the way.  One chunk pair a thread
+// and six CTAs an SM (40 registers) measured best: 10800 tokens of 80 heads, 442 MB in bf16, in
+// 72 us (0.94 of the copy rate), with four pairs a thread at two CTAs 92, with two at four 77; cos
+// and sin computed by each thread for a share of the heads, without shared memory, 81.
 #include "common.cuh"
 #include "kernels.h"
 #include "rope.cuh"
