@@ -251,8 +251,8 @@ __global__ void __launch_bounds__(kAqThreads, (ctas_per_sm<FMT, D, GROUP, NT>())
   static_assert(kAqRows % ROWS_AT_ONCE == 0 || ROWS_AT_ONCE % kAqRows == 0, "rows keep their unit");
   constexpr int SF = HEADS * G;                      // scales of a row
   const long long row_step = (long long)a.q.H * St::kRow, scale_step = (long long)a.q.H * 4 * G;
-  const bool wide = SF % 4 == 0 && scale_step % 16 == 0;  // scales in 16-byte vectors (else one by one)
-  const int piece = wide ? 4 : 1, pieces = SF / piece;
+  // ... in 16-byte vectors where they come in fours (H is a multiple of HEADS, so every row of them is aligned then)
+  constexpr int PIECE = SF % 4 == 0 ? 4 : 1, PIECES = SF / PIECE;
   int asked_tile = 0, slot = first / tiles_page, in_page = first - slot * tiles_page, known = -1;
   const char *kbase = nullptr, *vbase = nullptr;
   unsigned long long valid_of = 0;  // rows of the tiles asked for, 16 bits each, the next to be worked on first
@@ -295,17 +295,15 @@ __global__ void __launch_bounds__(kAqThreads, (ctas_per_sm<FMT, D, GROUP, NT>())
             v += ROWS_AT_ONCE * row_step;
           }
         }
-        for (int i = tid; i < TILE * pieces; i += kAqThreads) {
-          const int row = i / pieces, at = i - row * pieces;
-          const bool on = row < valid;
-          const long long src = a.q.scale_offset + (on ? (row0 + row) * scale_step + h0 * 4 * G + at * piece * 4 : 0);
-          const uint32_t to = dst + St::kKs + (row * SF + at * piece) * 4;
-          if (wide) {
-            cp_async_zero<16>(to, kbase + src, on);
-            cp_async_zero<16>(to + St::kScales, vbase + src, on);
-          } else {
-            cp_async_zero<4>(to, kbase + src, on);
-            cp_async_zero<4>(to + St::kScales, vbase + src, on);
+#pragma unroll
+        for (int i0 = 0; i0 < TILE * PIECES; i0 += kAqThreads) {
+          const int i = i0 + tid, row = i / PIECES, at = i % PIECES * PIECE;
+          if (i < TILE * PIECES) {
+            const bool on = row < valid;
+            const long long src = a.q.scale_offset + (on ? (row0 + row) * scale_step + (h0 * G + at) * 4 : 0);
+            const uint32_t to = dst + St::kKs + (row * SF + at) * 4;
+            cp_async_zero<4 * PIECE>(to, kbase + src, on);
+            cp_async_zero<4 * PIECE>(to + St::kScales, vbase + src, on);
           }
         }
       }
