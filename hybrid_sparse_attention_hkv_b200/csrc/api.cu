@@ -1037,6 +1037,16 @@ hsa_status_t hsa_rope_freqs(int dim, double base, int scaling, double factor, in
   return HSA_OK;
 }
 
+// Outputs may be their own inputs, element by element: not the same memory under other strides, nor another
+// tensor's.
+static hsa_status_t rope_alias(const char* fn, const char* what, const hsa::RowsArgs& in, const hsa::RowsArgs& out,
+                               int T, bool own) {
+  if (in.data != out.data) return HSA_OK;
+  if (!own || (T > 1 && in.token_stride != out.token_stride) || (in.H > 1 && in.head_stride != out.head_stride))
+    return fail(HSA_ERR_INVALID_ARG, "%s: %s start at one address (in place: a tensor's own input, same strides)", fn, what);
+  return HSA_OK;
+}
+
 static hsa_status_t rope_impl(const char* fn, const hsa_rope_t* rope, const int32_t* pos, long long pos_stride, int T,
                               int d, int dtype, const hsa_rows_t* q_in, const hsa_rows_t* q_out, const hsa_rows_t* k_in,
                               const hsa_rows_t* k_out, float sign, hsa_stream_t stream) {
@@ -1058,6 +1068,13 @@ static hsa_status_t rope_impl(const char* fn, const hsa_rope_t* rope, const int3
   hsa::RopeArgs r;
   TRY(rope_args(fn, rope, pos, pos_stride, T, d, sign, &r));
   if (T == 0) return HSA_OK;
+  TRY(rope_alias(fn, "q_in and q_out", qi, qo, T, true));
+  if (k_in) {
+    TRY(rope_alias(fn, "k_in and k_out", ki, ko, T, true));
+    TRY(rope_alias(fn, "q_in and k_out", qi, ko, T, false));
+    TRY(rope_alias(fn, "k_in and q_out", ki, qo, T, false));
+    TRY(rope_alias(fn, "q_out and k_out", qo, ko, T, false));
+  }
   HSA_LAUNCH("rope", hsa::launch_rope(r, T, d, dtype, qi, qo, ki, ko, stream));
   return HSA_OK;
 }

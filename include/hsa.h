@@ -430,7 +430,8 @@ hsa_status_t hsa_rope_freqs(int dim, double base, int scaling, double factor, in
 /* y = rotated x for the tokens' queries and, in the same pass, their keys (k_in and
  * k_out NULL: queries only).  pos: device int32 [n_axes][T] (rows pos_stride elements
  * apart, pos_stride >= T).  q_out / k_out may be q_in / k_in (in place, same strides);
- * other overlaps are not allowed.  T may be 0 (nothing is launched).  d in {64, 128}. */
+ * other overlaps are not allowed (outputs that start at another tensor's address, or at
+ * their input's with other strides, are refused).  T may be 0 (nothing is launched).  d in {64, 128}. */
 hsa_status_t hsa_rope(const hsa_rope_t* rope, const int32_t* pos, long long pos_stride, int T, int d, int dtype,
                       const hsa_rows_t* q_in, const hsa_rows_t* q_out, const hsa_rows_t* k_in,
                       const hsa_rows_t* k_out, hsa_stream_t stream);

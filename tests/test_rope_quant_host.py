@@ -132,8 +132,24 @@ def test_rope_refusals(lib, fn):
         assert call_rope(lib, fn) == 4 and "injected" in detail()
         # fp32 strides count in 4-byte elements, a broadcast input row is allowed
         assert call_rope(lib, fn, dtype=2, qi=rows(ts=132, hs=64), qo=rows(ts=132)) == 4
-        assert call_rope(lib, fn, qi=rows(ts=0)) == 4
-        assert call_rope(lib, fn, qo=rows(ts=64, hs=256)) == 4  # [H, T, d]
+        assert call_rope(lib, fn, qi=rows(data=0x20000, ts=0)) == 4
+        assert call_rope(lib, fn, qo=rows(data=0x20000, ts=64, hs=256)) == 4  # [H, T, d]
+
+
+@pytest.mark.parametrize("fn", ["hsa_rope", "hsa_rope_bwd"])
+def test_rope_refuses_outputs_over_other_elements(lib, fn):
+    B = 0x20000
+    for kw in (dict(qi=rows(ts=0)), dict(qi=rows(ts=256)), dict(qo=rows(ts=64, hs=256)),     # one address, other strides
+               dict(ki=rows(data=B), ko=rows(data=B, ts=256)),
+               dict(ki=rows(data=B), ko=rows()), dict(qo=rows(data=B), ki=rows(data=B), ko=rows(data=0x30000)),
+               dict(qi=rows(data=0x30000), qo=rows(data=B), ki=rows(data=0x40000), ko=rows(data=B))):
+        assert call_rope(lib, fn, **kw) == 1 and "one address" in detail(), kw
+    with hsa.injected_fault(hsa.FAULT_LAUNCH):
+        # in place; queries and keys of one buffer; one row whatever its stride; one head whatever its stride; shared inputs
+        for kw in (dict(ki=rows(data=B), ko=rows(data=B)), dict(ki=rows(data=A + 256, ts=256), ko=rows(data=A + 256, ts=256)),
+                   dict(T=1, qi=rows(ts=0)), dict(qi=rows(H=1, hs=64), qo=rows(H=1, hs=128)),
+                   dict(qo=rows(data=B), ki=rows(), ko=rows(data=0x30000))):
+            assert call_rope(lib, fn, **kw) == 4, (kw, detail())
 
 
 def call_rows(lib, q=(0, 64), K=None, V=None, T=4, d=64, dtype=0, rope=None, pos=None, pos_stride=4, pk=P(A), pv=P(A), NP=2,
