@@ -1093,6 +1093,15 @@ hsa_status_t hsa_rope_bwd(const hsa_rope_t* rope, const int32_t* pos, long long 
 
 // ------------------------------------------------------------------ quantised pages
 
+// A call's page tables, and its selection where it has one.
+static hsa_status_t check_pages(const char* fn, const void* page_k, const void* page_v, const int32_t* sel, bool has_sel) {
+  if (!page_k || !page_v || (has_sel && !sel)) return fail(HSA_ERR_INVALID_ARG, "%s: NULL page table or selection", fn);
+  if (((reinterpret_cast<uintptr_t>(page_k) | reinterpret_cast<uintptr_t>(page_v)) & 7u) != 0 ||
+      (reinterpret_cast<uintptr_t>(sel) & 3u) != 0)
+    return fail(HSA_ERR_INVALID_ARG, "%s: a page table is not 8-byte aligned, or the selection not 4-byte aligned", fn);
+  return HSA_OK;
+}
+
 static hsa_status_t quant_args(const char* fn, const hkv_quant_t* q, int P_tok, int H, int d, hsa::QuantArgs* out) {
   if (t_fault == HSA_FAULT_ARG) return fail(HSA_ERR_INVALID_ARG, "%s: injected argument failure", fn);
   if (!q) return fail(HSA_ERR_INVALID_ARG, "%s: quant is NULL", fn);
@@ -1142,7 +1151,7 @@ hsa_status_t hkv_quant_rows(const hkv_quant_t* q, const hsa_rows_t* K, const hsa
   hsa::RopeArgs r;
   TRY(rope_args(fn, rope, pos, pos_stride, T, d, 1.f, &r));
   if (NP < 1) return fail(HSA_ERR_INVALID_ARG, "%s: NP = %d must be >= 1", fn, NP);
-  if (!page_k || !page_v) return fail(HSA_ERR_INVALID_ARG, "%s: NULL page table", fn);
+  TRY(check_pages(fn, page_k, page_v, nullptr, false));
   if (!first_row_dev && (first_row < 0 || first_row > (long long)NP * P_tok - T))
     return fail(HSA_ERR_INVALID_ARG, "%s: rows [%lld, %lld) outside the %d pages of %d", fn, first_row, first_row + T, NP,
                 P_tok);
@@ -1167,7 +1176,7 @@ hsa_status_t hkv_gather_quant(const hkv_quant_t* q, const void* const* page_k, c
   if (Kp < 1 || Kp > NP) return fail(HSA_ERR_INVALID_ARG, "%s: Kp = %d must be in [1, NP]", fn, Kp);
   if ((long long)Kp * P_tok > 0x7fffffffLL)
     return fail(HSA_ERR_UNSUPPORTED, "%s: Kp * P_tok = %lld rows exceed 2^31 - 1", fn, (long long)Kp * P_tok);
-  if (!page_k || !page_v || !sel) return fail(HSA_ERR_INVALID_ARG, "%s: NULL page table or selection", fn);
+  TRY(check_pages(fn, page_k, page_v, sel, true));
   REQUIRE_PTR(Kc);
   REQUIRE_PTR(Vc);
   OPTIONAL_PTR(kbar128);
@@ -1218,8 +1227,10 @@ hsa_status_t hkv_attn_quant(const hkv_quant_t* q, const hsa_bf16* Q, int T, int 
   size_t part_ml, total;
   TRY(attn_quant_layout(fn, T, Hq, H, d, Kp, P_tok, &a.splits, &part_ml, &total));
   if (NP < 1 || Kp > NP) return fail(HSA_ERR_INVALID_ARG, "%s: Kp = %d must be in [1, NP = %d]", fn, Kp, NP);
-  if (!page_k || !page_v || !sel) return fail(HSA_ERR_INVALID_ARG, "%s: NULL page table or selection", fn);
+  TRY(check_pages(fn, page_k, page_v, sel, true));
   if (!(scale >= 0.f) || isinf(scale)) return fail(HSA_ERR_INVALID_ARG, "%s: scale must be finite and >= 0", fn);
+  if (((reinterpret_cast<uintptr_t>(n_rows) | reinterpret_cast<uintptr_t>(lse)) & 3u) != 0)
+    return fail(HSA_ERR_INVALID_ARG, "%s: n_rows and lse must be 4-byte aligned", fn);
   TRY(check_ws(fn, ws, ws_bytes, total));
   if (T == 0) return HSA_OK;
   REQUIRE_PTR(Q);

@@ -223,6 +223,20 @@ def test_attn_quant_refusals(lib):
         hsa.hkv_attn_quant_workspace_size(65, 1, 1, 64, 1, 16)
 
 
+def test_tables_selections_and_lengths_are_aligned(lib):
+    ODD = P(0x10002)
+    for kw in (dict(pk=P(MIS)), dict(pv=P(MIS))):
+        assert call_rows(lib, **kw) == 1 and "aligned" in detail(), kw
+        assert call_gather(lib, **kw) == 1 and "aligned" in detail(), kw
+        assert call_attn(lib, **kw) == 1 and "aligned" in detail(), kw
+    assert call_gather(lib, sel=ODD) == 1 and "aligned" in detail()
+    for kw in (dict(sel=ODD), dict(n=ODD), dict(lse=ODD)):
+        assert call_attn(lib, **kw) == 1 and "aligned" in detail(), kw
+    with hsa.injected_fault(hsa.FAULT_LAUNCH):  # 4 bytes are enough for a selection, a length and an lse
+        assert call_gather(lib, sel=P(MIS)) == 4
+        assert call_attn(lib, sel=P(MIS), n=P(MIS), lse=P(MIS)) == 4
+
+
 def test_binding_refuses_what_the_library_cannot_see(lib):
     """Types, shapes, strides and devices of the tensors are checked before their addresses are taken."""
     q = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
