@@ -35,6 +35,15 @@ class HkvHsaStep:
         quant (make_quant): the pages are quantised (with `store`, a QuantPageStore).
         rope, pos (make_rope; int32 [n_axes, Kp * P_tok]): their keys are rotated as they
         are read, to their places in the active cache; Q and Kq come rotated (hsa_rope)."""
+        held = getattr(store, "quant", None)
+        if store is not None and (held is None) != (quant is None):
+            raise ValueError(f"the store's pages are {'bf16' if held is None else 'quantised'}, the step's are "
+                             f"{'bf16' if quant is None else 'quantised'}")
+        if held is not None and ((held.format, held.group) != (quant.format, quant.group) or
+                                 (store.NP, store.rows, store.heads, store.head_dim) != (NP, P_tok, H, d)):
+            raise ValueError("the store's pages have another format or shape than the step's")
+        if rope is not None and quant is None:
+            raise ValueError("keys are rotated on the way from quantised pages only (quant is None)")
         self.H, self.d, self.Lq, self.P_tok, self.NP, self.Kp, self.rank = H, d, Lq, P_tok, NP, Kp, rank
         self.store = store
         self.Lc = Kp * P_tok
@@ -57,8 +66,6 @@ class HkvHsaStep:
         # Quantised pages are read with their block means instead: the sums of the sealed
         # keys are not those of the keys as they are read.
         self.quant, self.rope, self.pos = quant, rope, pos
-        if rope is not None and quant is None:
-            raise ValueError("keys are rotated on the way from quantised pages only (quant is None)")
         self.early = P_tok % 64 == 0 and quant is None
         self.sums64 = torch.zeros(NP, P_tok // 64, H, d, dtype=torch.float32, device=dev) if self.early else None
         self.gather_stream = torch.cuda.Stream(device=dev) if self.early else None

@@ -223,6 +223,24 @@ def test_attn_quant_refusals(lib):
         hsa.hkv_attn_quant_workspace_size(65, 1, 1, 64, 1, 16)
 
 
+def test_a_step_refuses_a_store_of_other_pages():
+    """Reading pages of one format as another's runs over their ends, so the step looks before it allocates anything."""
+    from hybrid_sparse_attention_hkv_b200.step import HkvHsaStep
+    from hybrid_sparse_attention_hkv_b200.store import PageStore, QuantPageStore
+    held = QuantPageStore.__new__(QuantPageStore)
+    held.quant, held.NP, held.rows, held.heads, held.head_dim = hsa.make_quant(0, 64), 4, 256, 2, 64
+    plain = PageStore.__new__(PageStore)
+
+    def step(store, quant, H=2, d=64, P_tok=256, NP=4):
+        return HkvHsaStep(H, d, 256, P_tok, NP, 2, 64, None, None, device="cpu", store=store, quant=quant)
+    for store, quant, kw in ((held, None, {}), (plain, hsa.make_quant(0, 64), {}), (held, hsa.make_quant(1, 64), {}),
+                             (held, hsa.make_quant(0, 32), {}), (held, hsa.make_quant(0, 64), dict(P_tok=512)),
+                             (held, hsa.make_quant(0, 64), dict(H=4)), (held, hsa.make_quant(0, 64), dict(d=128)),
+                             (held, hsa.make_quant(0, 64), dict(NP=8))):
+        with pytest.raises(ValueError, match="store's pages"):
+            step(store, quant, **kw)
+
+
 def test_tables_selections_and_lengths_are_aligned(lib):
     ODD = P(0x10002)
     for kw in (dict(pk=P(MIS)), dict(pv=P(MIS))):
