@@ -108,8 +108,13 @@ class QuantPageStore(PageStore):
         at = torch.arange(NP, dtype=torch.int64) * self.page_bytes
         self.host_tables = tuple((at + h.dev_ptr).to(self.slot_k.device) for h in self.host)
 
+    def _open(self, call):
+        if self.host is None:
+            _refuse(f"QuantPageStore.{call}", "the store is closed: its host tier is gone")
+
     def write(self, K, V, first_row: int, ws, first_row_dev=None, rope=None, pos=None, stream=None):
         """Append rows K, V [T, H, d] at history row first_row (+ first_row_dev): hkv_quant_rows into the host tier."""
+        self._open("write")
         hkv_quant_rows(self.quant, K, V, *self.host_tables, self.rows, first_row, ws, first_row_dev, rope, pos, stream)
 
     def seal(self, page: int, K_rows, V_rows, kbar_out, ws, rope=None, pos=None, stream=None):
@@ -124,10 +129,12 @@ class QuantPageStore(PageStore):
 
     def gather(self, sel, Kc, Vc, ws, kbar128=None, rope=None, pos=None, stream=None):
         """hkv_gather_quant of the pages `sel` (int32 device tensor), from their slots or the host tier."""
+        self._open("gather")
         hkv_gather_quant(self.quant, *self.page_tables(), sel, sel.numel(), self.rows, self.heads, self.head_dim, Kc, Vc, ws,
                          kbar128, rope, pos, stream)
 
     def attend(self, Q, sel, out, lse, ws, n_rows=None, scale=0.0, stream=None):
         """hkv_attn_quant of a few queries over the pages `sel`."""
+        self._open("attend")
         hkv_attn_quant(self.quant, Q, *self.page_tables(), sel, sel.numel(), self.rows, self.heads, out, lse, ws, n_rows, scale,
                        stream)

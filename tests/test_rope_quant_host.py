@@ -241,6 +241,20 @@ def test_a_step_refuses_a_store_of_other_pages():
             step(store, quant, **kw)
 
 
+def test_a_closed_quantised_store_is_not_read_or_written():
+    from hybrid_sparse_attention_hkv_b200.store import QuantPageStore
+    s = QuantPageStore.__new__(QuantPageStore)
+    s._own, s.host = False, (None, None)
+    s.quant, s.NP, s.rows, s.heads, s.head_dim = hsa.make_quant(0, 64), 2, 4, 1, 64
+    s.close()
+    x = torch.zeros(4, 1, 64, dtype=torch.bfloat16)
+    sel, ws = torch.zeros(1, dtype=torch.int32), torch.zeros(256, dtype=torch.uint8)
+    for call in (lambda: s.write(x, x, 0, ws), lambda: s.seal(0, x, x, x, ws), lambda: s.gather(sel, x, x, ws),
+                 lambda: s.attend(x, sel, x, None, ws)):
+        with pytest.raises(hsa.HsaError, match="closed"):
+            call()
+
+
 def test_tables_selections_and_lengths_are_aligned(lib):
     ODD = P(0x10002)
     for kw in (dict(pk=P(MIS)), dict(pv=P(MIS))):
