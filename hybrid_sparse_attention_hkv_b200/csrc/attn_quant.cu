@@ -355,8 +355,9 @@ __global__ void __launch_bounds__(kAqThreads, (ctas_per_sm<FMT, D, GROUP, NT>())
       qf[n][k][0] = pack_half2(v[4 * k] * inv, v[4 * k + 1] * inv);
       qf[n][k][1] = pack_half2(v[4 * k + 2] * inv, v[4 * k + 3] * inv);
     }
-    qs[n][0] = __shfl_sync(0xffffffffu, unit, 8 * t) * a.scale_log2e;
-    qs[n][1] = __shfl_sync(0xffffffffu, unit, 8 * t + 4) * a.scale_log2e;
+    // (kept above 0: -inf times it is to be -inf; what 2^-149 makes of a score of any size is below 2^-21)
+    qs[n][0] = fmaxf(__shfl_sync(0xffffffffu, unit, 8 * t) * a.scale_log2e, __uint_as_float(1u));
+    qs[n][1] = fmaxf(__shfl_sync(0xffffffffu, unit, 8 * t + 4) * a.scale_log2e, __uint_as_float(1u));
   }
 
   float o[NT][G * KS][4];

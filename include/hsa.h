@@ -507,9 +507,9 @@ hsa_status_t hkv_gather_quant(const hkv_quant_t* q, const void* const* page_k, c
  * (n_rows: optional device int32; NULL: all rows), with k_r, v_r of key head
  * h / (Hq / H).  Keys are used as stored (rotate them as they are written).  Q:
  * [T, Hq, d] bf16, Hq a multiple of H; out: [T, Hq, d] fp32, or bf16 when out_is_bf16;
- * lse (optional): [T, Hq] fp32.  scale: 0 means 1/sqrt(d).  n = 0 gives o = 0 and lse =
- * -inf; a bad page sets HSA_ERR_DEVICE and its rows are not attended to.  Two results
- * over disjoint rows merge by their lse.  T <= 64; for a whole chunk assemble the cache
+ * lse (optional): [T, Hq] fp32.  scale: 0 means 1/sqrt(d).  Scores beyond fp32's range
+ * give NaN.  n = 0 gives o = 0 and lse = -inf; a bad page sets HSA_ERR_DEVICE and its rows
+ * are not attended to.  Two results over disjoint rows merge by their lse.  T <= 64; for a whole chunk assemble the cache
  * and use hsa_forward.  T may be 0.  Deterministic.  Workspace:
  * hkv_attn_quant_workspace_size() bytes, its 256-byte header as every workspace's. */
 hsa_status_t hkv_attn_quant_workspace_size(int T, int Hq, int H, int d, int Kp, int P_tok, size_t* bytes);

@@ -436,6 +436,23 @@ def test_attention_query_magnitudes():
     within(out[0, 0], v[top, 0], 2.0 ** -20 * v.abs().max())
 
 
+@pytest.mark.parametrize("T", [5, 12])
+def test_attention_scales_below_the_exponent_range(T):
+    """Zero and tiny queries with scales whose product with them is below fp32's range: the rows' plain mean, also where a
+    tile's last rows are masked."""
+    q, H, d, P = hsa.make_quant(0, 64), 2, 64, 150
+    pk, pv = filled(q, 2, P, H, d, 152), filled(q, 2, P, H, d, 153)
+    n = 2 * P - 7
+    k, v = (p.rows64().flatten(0, 1)[:n] for p in (pk, pv))
+    Q = rand(T, H, d, seed=154, dtype=torch.bfloat16)
+    Q[0] = 0
+    Q[1] *= 1e-36
+    for scale in (1e-9, 1e-20, 1e-38):
+        out, ls, st = attend(q, Q, pk, pv, [0, 1], n_rows=n, scale=scale)
+        assert st == 0
+        check_attention(out, ls, Q, k, v, torch.tensor(scale).item())
+
+
 def test_attention_not_finite_groups_reach_their_own_head_only():
     q, H, d, P = hsa.make_quant(0, 64), 3, 64, 40
     for which in ("k", "v"):
