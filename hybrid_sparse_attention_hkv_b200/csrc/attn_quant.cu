@@ -123,7 +123,7 @@ inline int attn_quant_heads(int H) { return H % 4 == 0 ? 4 : H % 2 == 0 ? 2 : 1;
 // Splits of the rows: one wave of CTAs, at least a tile to each.
 inline int attn_quant_splits_of(int ctas_per_sm, int T, int Hq, int H, int Kp, int P_tok) {
   const int cols = T * (Hq / H), heads = attn_quant_heads(H), tile = kAqRows * kAqWarps / heads;
-  const long long tiles = (long long)Kp * ((P_tok + tile - 1) / tile);
+  const long long tiles = (long long)Kp * ((P_tok - 1) / tile + 1);
   const long long units = (long long)(H / heads) * (cols <= 8 ? 1 : (cols + 15) / 16);
   long long n = 148LL * ctas_per_sm / units;
   if (n > tiles) n = tiles;
@@ -229,10 +229,10 @@ __global__ void __launch_bounds__(kAqThreads, (ctas_per_sm<FMT, D, GROUP, NT>())
   const long long all = (long long)a.Kp * P;
   long long n_rows = a.n_rows ? (long long)*a.n_rows : all;
   n_rows = n_rows < 0 ? 0 : (n_rows > all ? all : n_rows);
-  const int tiles_page = (P + TILE - 1) / TILE;
+  const int tiles_page = (P - 1) / TILE + 1;
   const int whole = (int)(n_rows / P), rest = (int)(n_rows - (long long)whole * P);
-  const int tiles = whole * tiles_page + (rest + TILE - 1) / TILE;
-  const int per = (tiles + a.splits - 1) / a.splits;
+  const int tiles = whole * tiles_page + rest / TILE + (rest % TILE != 0);
+  const int per = tiles / a.splits + (tiles % a.splits != 0);
   const int first = (int)min((long long)tiles, (long long)split * per), rounds = min(per, tiles - first);
 
   // asking for tiles: a row's codes are HEADS * kRow bytes next to each other, its scales
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kAqThreads, (ctas_per_sm<FMT, D, GROUP, NT>())
         const int row0 = in_page * TILE;
         valid = min((slot < whole ? P : rest) - row0, TILE);
         const uint32_t dst = ring_s + stage * St::kBytes, to = dst + my_place;
-        const long long from = (row0 + my_row) * row_step + h0 * St::kRow + my_vec * 16;
+        const long long from = ((long long)row0 + my_row) * row_step + h0 * St::kRow + my_vec * 16;
         const char *k = kbase + from, *v = vbase + from;
         if (valid == TILE) {
 #pragma unroll

@@ -244,9 +244,9 @@ ReadArgs::Part read_part(const ReadArgs& a, bool pool) {
   p.slab = (a.q.H + p.slabs - 1) / p.slabs;
   p.phases = kReadThreads / (p.slab * J);
   int rounds = p.phases < kReadRows / kReadRounds ? kReadRows / p.phases : kReadRounds;
-  while (rounds > 1 && a.Lc / (p.phases * rounds) * p.slabs < 2 * 148) --rounds;
+  while (rounds > 1 && 1LL * a.Lc / (p.phases * rounds) * p.slabs < 2 * 148) --rounds;
   p.rows = pool ? 128 : p.phases * rounds;
-  while (p.slabs < a.q.H && ((a.Lc - 1) / p.rows + 1) * p.slabs < 148) p.slabs = min(2 * p.slabs, a.q.H);
+  while (p.slabs < a.q.H && ((a.Lc - 1) / p.rows + 1LL) * p.slabs < 148) p.slabs = min(2 * p.slabs, a.q.H);
   p.slab = (a.q.H + p.slabs - 1) / p.slabs;
   p.slabs = (a.q.H + p.slab - 1) / p.slab;
   p.phases = kReadThreads / (p.slab * J);
@@ -257,7 +257,7 @@ ReadArgs::Part read_part(const ReadArgs& a, bool pool) {
 
 template <int FMT, int J, int ROPE, bool POOL>
 cudaError_t launch_read(ReadArgs& a, cudaStream_t s) {
-    a.k = read_part<J>(a, POOL);
+  a.k = read_part<J>(a, POOL);
   a.v = read_part<J>(a, false);
   const int need = max(a.k.slab * a.k.phases, a.v.slab * a.v.phases) * J;
   const int threads = max(8 * J, (need + 31) / 32 * 32);  // 8 J: the cos and sin of a row

@@ -255,6 +255,11 @@ def test_a_closed_quantised_store_is_not_read_or_written():
             call()
 
 
+def test_the_longest_caches_are_split_like_long_ones(lib):
+    size = lambda *a: hsa.hkv_attn_quant_workspace_size(1, 2, 2, 64, *a)  # noqa: E731
+    assert size(1, 2 ** 31 - 1) == size(1, 2 ** 31 - 1024) == size(2 ** 31 - 1, 1) == size(2 ** 20, 2 ** 10) > 256
+
+
 def test_tables_selections_and_lengths_are_aligned(lib):
     ODD = P(0x10002)
     for kw in (dict(pk=P(MIS)), dict(pv=P(MIS))):
