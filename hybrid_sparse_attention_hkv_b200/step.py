@@ -34,7 +34,9 @@ class HkvHsaStep:
         then followed by the store's fetch (the selected pages made resident in HBM).
         quant (make_quant): the pages are quantised (with `store`, a QuantPageStore).
         rope, pos (make_rope; int32 [n_axes, Kp * P_tok]): their keys are rotated as they
-        are read, to their places in the active cache; Q and Kq come rotated (hsa_rope)."""
+        are read, to their places in the active cache; Q and Kq come rotated (hsa_rope),
+        and the page retrieval, whose summaries are of the keys before their rotation,
+        takes the queries before theirs (`q_pages` of the calls; None: Q)."""
         held = getattr(store, "quant", None)
         if store is not None and (held is None) != (quant is None):
             raise ValueError(f"the store's pages are {'bf16' if held is None else 'quantised'}, the step's are "
@@ -95,7 +97,7 @@ class HkvHsaStep:
                        self.ws, self.kbar128)
 
     def __call__(self, Q, Kq, Vq, tau, gate_logit, E, F, e_cur=None, e_seg=None, seg_begin=None,
-                 ef_head_stride=0, out=None):
+                 ef_head_stride=0, out=None, q_pages=None):
         """One step on the current stream; the result goes to `out` (same shape and
         dtype as self.out) when given, else to self.out."""
         dst = self.out if out is None else out
@@ -103,7 +105,7 @@ class HkvHsaStep:
         if e_cur is not None:
             hkv_select_prompt(e_cur, e_seg, seg_begin, self.seg, self.cand_range)
             cand = self.cand_range
-        self._retrieve(Q, cand)
+        self._retrieve(Q if q_pages is None else q_pages, cand)
         if self.store is not None:
             self.store.fetch(self.sel, self.ws)
         if not self.early:
@@ -128,14 +130,14 @@ class HkvHsaStep:
         return dst
 
     # ------------------------------------------------------------ multi-step reuse
-    def prepare_chunk(self, Q, E, F, e_cur=None, e_seg=None, seg_begin=None, ef_head_stride=0):
+    def prepare_chunk(self, Q, E, F, e_cur=None, e_seg=None, seg_begin=None, ef_head_stride=0, q_pages=None):
         """Once per chunk: retrieval (prompt-level, page-level) with the chunk's queries,
         the gather of the active cache, and the cached KV's Linformer products."""
         cand = None
         if e_cur is not None:
             hkv_select_prompt(e_cur, e_seg, seg_begin, self.seg, self.cand_range)
             cand = self.cand_range
-        self._retrieve(Q, cand)
+        self._retrieve(Q if q_pages is None else q_pages, cand)
         if self.store is not None:
             self.store.fetch(self.sel, self.ws)
         self._gather()

@@ -180,6 +180,35 @@ def test_step_over_quantised_pages(layout, use_store):
             store.close()
 
 
+def test_step_retrieves_pages_by_the_queries_before_their_rotation():
+    """A page whose keys point along the queries is found whatever the chunk's positions; queries that are half a turn
+    further point the other way, and would retrieve the wrong pages."""
+    quant, H, d, Lq, P, NP, Kp, r = hsa.make_quant(1, 64), 2, 64, 256, 256, 6, 2, 64
+    inv = torch.full((d // 2,), math.pi / 8, dtype=torch.float64, device="cuda")
+    rope = hsa.make_rope(inv, hsa.ROPE_HALF)
+    toward = torch.from_numpy(np.sign(np.arange(d) % 3 - 0.5).astype(np.float32)).cuda().bfloat16()
+    K = torch.stack([toward * (c + 0.5) for c in (-1, 0.5, 2, -2, 1, -3)])[:, None, None].expand(NP, P, H, d).contiguous()
+    V = to_dev(synth.normal_bf16((NP, P, H, d), 63, 1))
+    Q = (toward + 0.25 * to_dev(synth.normal_bf16((Lq, H, d), 63, 2))).bfloat16()
+    Kq, Vq = (to_dev(synth.normal_bf16((Lq, H, d), 63, i)) for i in (3, 4))
+    E, F = (to_dev(synth.normal_bf16((r, Kp * P + Lq), 63, i, sigma=1 / math.sqrt(r))) for i in (5, 6))
+    tau, z = torch.full((H,), 0.9, device="cuda"), torch.zeros(H, device="cuda")
+    pages = Pages(hsa, quant, NP, P, H, d), Pages(hsa, quant, NP, P, H, d)
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    hsa.hkv_quant_rows(quant, K.flatten(0, 1), V.flatten(0, 1), pages[0].table, pages[1].table, P, 0, ws)
+    pos_c, pos_q = (torch.full((n,), p, dtype=torch.int32, device="cuda") for n, p in ((Kp * P, 0), (Lq, 8)))
+    step = HkvHsaStep(H, d, Lq, P, NP, Kp, r, pages[0].table, pages[1].table, quant=quant, rope=rope, pos=pos_c)
+    step.seal_pages(K)
+    Qr = torch.empty_like(Q)
+    hsa.hsa_rope(rope, pos_q, Q, Qr)
+    step(Qr, Kq, Vq, tau, z, E, F, q_pages=Q)
+    assert step.sel.tolist() == [2, 4]
+    step.prepare_chunk(Qr, E, F, q_pages=Q)
+    assert step.sel.tolist() == [2, 4]
+    step(Qr, Kq, Vq, tau, z, E, F)
+    assert step.sel.tolist() == [3, 5]
+
+
 def test_step_refuses_a_rotation_of_bf16_pages():
     inv = hsa.rope_freqs(64)[0].cuda()
     t = torch.zeros(4, dtype=torch.int64, device="cuda")
