@@ -436,6 +436,21 @@ def test_attention_query_magnitudes():
     within(out[0, 0], v[top, 0], 2.0 ** -20 * v.abs().max())
 
 
+@pytest.mark.parametrize("fmt", [0, 1, 2])
+@pytest.mark.parametrize("d,group", [(64, 32), (64, 64), (128, 32), (128, 64), (128, 128)])
+@pytest.mark.parametrize("T,g,H,P,sel,n", [(1, 1, 4, 33, [1, 1, 0], 70), (3, 4, 8, 95, [2, 0, 2], None), (9, 1, 6, 64, [0, 0], 127),
+                                           (64, 1, 4, 5, [2, 2, 2], 14)])
+def test_attention_of_neighbouring_heads_and_pages_selected_twice(T, g, H, P, sel, n, d, group, fmt):
+    q = hsa.make_quant(fmt, group)
+    pk, pv = filled(q, 3, P, H, d, 140), filled(q, 3, P, H, d, 141)
+    Q = rand(T, H * g, d, seed=142, dtype=torch.bfloat16)
+    rows = len(sel) * P if n is None else n
+    k, v = (p.rows64()[sel].flatten(0, 1)[:rows] for p in (pk, pv))
+    out, ls, st = attend(q, Q, pk, pv, sel, n_rows=n)
+    assert st == 0
+    check_attention(out, ls, Q, k, v, 1 / math.sqrt(d))
+
+
 @pytest.mark.parametrize("T", [5, 12])
 def test_attention_scales_below_the_exponent_range(T):
     """Zero and tiny queries with scales whose product with them is below fp32's range: the rows' plain mean, also where a
