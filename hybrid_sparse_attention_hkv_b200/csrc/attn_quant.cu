@@ -17,10 +17,19 @@
 //   q    bf16 has 8 significant bits; scaled per query by a power of two to magnitudes
 //        below 2 it is exact in fp16 down to 2^-24 of the query's largest element (less
 //        is rounded at 2^-25 of it);
-//   w    is split into two halves, w = hi + lo, with an error of 2^-22 of w, or 2^-24 of
-//        the largest weight for small ones.  To stay within fp16's range, value scales
-//        are taken relative to a running power of two per group (`vref`), which only rises;
-//        the accumulators are rescaled when it does, as when the running maximum rises.
+//   w    enters as two halves: what a half holds of it, and what that leaves, 2^12 times as
+//        large, in a product of its own.  For each 32 keys, query and group, w is scaled by the
+//        power of two that brings the largest to [2^14, 2^15): every w down to 2^-28 of it enters
+//        with an error below 2^-23 of its own, smaller ones with one below 2^-51 of the largest.
+//        A large value scale on a key with little weight, or a key with all the weight and a
+//        value of zero, costs the others nothing.
+// The products of 16 or 32 keys go to accumulators of their own and are added to O by fp32 FMAs:
+// the tensor core's adder cuts off what a long sum does not hold (one token over 49920 rows: off by
+// 2e-7 of the output; 8e-7 with one accumulator for all rows).
+// Weights in three parts of bf16, which need no scaling, measured 39 us for one token over 49920
+// rows of 12 heads against 37 (codes cost three times as much to turn into bf16), without the
+// FMAs.  One running power of two for a group's value scales took 36, but left small weights
+// beside a large scale, or behind a large weight, without their bits.
 //
 // Work: a CTA takes tiles of a split of the rows, four warps with 32 keys of a head each: of
 // four neighbouring heads where there are so many, so that a row's codes are fetched in runs of
@@ -28,14 +37,15 @@
 // from each 32-byte sector, were half of all requests: 124 us instead of 96 for one token over
 // 49920 rows of 40 heads).  Tiles are on their way to a ring in shared memory while one is
 // worked on; small CTAs, three to an SM, drift apart and keep the loads going where one of 8 or
-// 12 warps stops at its barrier (199680 rows: 329 us, 0.98 of the copy rate, against 395 to
-// 425).  The splits are joined by a second kernel in order (deterministic).  A tile never
-// straddles pages; what lies behind a page's or the cache's end is fetched as zeros and gets no
-// weight.
+// 12 warps stops at its barrier (before the weights took their present form 329 us for 199680 rows
+// of 40 heads against 395 to 425; 380 with it, 0.85 of the copy rate).  The splits are joined by a
+// second kernel in order (deterministic).  A tile never straddles pages; what lies behind a page's
+// or the cache's end is fetched as zeros and gets no weight.
 //
 // Short caches are bound by their latency: two launches, the way from the row count to the page
-// table to the rows, and the join cost 9 us together.  4-bit codes are bound by the instructions
-// that turn them into operands (49920 rows of 12 heads: 36 us against 37 us in 8 bits).
+// table to the rows, and the join cost 9 us together.  4-bit codes, and groups of 32 columns, are
+// bound by instructions: turning codes into operands, and scaling and splitting the weights for each
+// group (49920 rows of 12 heads of 128 columns in 8 bits, 4 bits, 8 bits in groups of 32: 37, 37 and 49 us).
 #include "common.cuh"
 #include "kernels.h"
 #include "quant.cuh"
@@ -90,6 +100,28 @@ __device__ __forceinline__ void nibbles(uint32_t w, uint32_t& p0, uint32_t& p1) 
                             *reinterpret_cast<const __half2*>(&minus72));
   p1 = *reinterpret_cast<const uint32_t*>(&y);
 }
+
+// The upper halves, or the lower ones, of two words: a's below b's.
+__device__ __forceinline__ uint32_t upper_halves(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7632); }
+__device__ __forceinline__ uint32_t lower_halves(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x5410); }
+
+// Two fp32 operations in one instruction, each rounded to nearest.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{.reg .b64 w, x, y, z;\n\tmov.b64 w, {%2, %3};\n\tmov.b64 x, {%4, %5};\n\tmov.b64 y, {%6, %7};\n\t"
+      "fma.rn.f32x2 z, w, x, y;\n\tmov.b64 {%0, %1}, z;}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 // N bytes of codes a thread reads at once, as words (N = 2: the low half of one).
 template <int N>
@@ -178,6 +210,10 @@ __device__ __forceinline__ float exp2_approx(float x) {
 __device__ __forceinline__ float pow2_below(float x) {  // the power of two at or below x, within [2^-126, 2^126]
   const uint32_t e = min(max(__float_as_uint(x) >> 23, 1u), 253u);
   return __uint_as_float(e << 23);
+}
+// The power of two that brings weights of at most x to below 2^15: within [2^-126, 2^114].
+__device__ __forceinline__ float weight_unit(float x) {
+  return __uint_as_float((uint32_t)max((int)(__float_as_uint(x) >> 23) - 14, 1) << 23);
 }
 __device__ __forceinline__ float pow2_inverse(float p) { return __uint_as_float((254u << 23) - __float_as_uint(p)); }
 
@@ -362,9 +398,8 @@ __global__ void __launch_bounds__(kAqThreads, (ctas_per_sm<FMT, D, GROUP, NT>())
 
   float o[NT][G * KS][4];
   // the references that products are taken relative to (before qs, so that the largest differs
-  // from itself by nothing) and the value scales of each group: raised when something in a tile is
-  // more than 2^6 above them, so that weights stay below 2^12
-  float m[NT][2], ref[NT][2], high_at[NT][2], l[NT][2], vref[G];
+  // from itself by nothing): raised when something in a tile is more than 2^6 above them
+  float m[NT][2], ref[NT][2], high_at[NT][2], l[NT][2];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -374,8 +409,6 @@ __global__ void __launch_bounds__(kAqThreads, (ctas_per_sm<FMT, D, GROUP, NT>())
     high_at[n][0] = high_at[n][1] = -INFINITY;  // m + 6 / qs: what a product has to be above
     l[n][0] = l[n][1] = 0.f;
   }
-#pragma unroll
-  for (int i = 0; i < G; ++i) vref[i] = pow2_below(0.f);
 
   for (int i = 0, stage = 0; i < rounds; ++i, stage = stage == kAqStages - 1 ? 0 : stage + 1) {
     cp_async_wait<kAqStages - 2>();
@@ -426,8 +459,6 @@ __global__ void __launch_bounds__(kAqThreads, (ctas_per_sm<FMT, D, GROUP, NT>())
           for (int e = 0; e < 4; ++e)
             if (16 * mi + g + 8 * (e >> 1) >= valid) s[mi][n][e] = -INFINITY;
     }
-    // value scales of keys g and g + 8, and whether a reference has to be raised
-    float vs[M][2][G];
     bool high = false;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -438,19 +469,10 @@ __global__ void __launch_bounds__(kAqThreads, (ctas_per_sm<FMT, D, GROUP, NT>())
         for (int mi = 1; mi < M; ++mi) top = fmaxf(top, fmaxf(s[mi][n][e], s[mi][n][2 + e]));
         high |= top > high_at[n][e];
       }
-#pragma unroll
-    for (int mi = 0; mi < M; ++mi)
-#pragma unroll
-      for (int r = 0; r < 2; ++r)
-#pragma unroll
-        for (int k = 0; k < G; ++k) {
-          vs[mi][r][k] = v_scale[(16 * mi + g + 8 * r) * SF + k];
-          high |= fabsf(vs[mi][r][k]) > 64.f * vref[k];
-        }
     if (__any_sync(0xffffffffu, high)) {
-      float alpha[NT][2];
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NT; ++n) {
+        float alpha[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           float top = m[n][e];
@@ -460,70 +482,120 @@ __global__ void __launch_bounds__(kAqThreads, (ctas_per_sm<FMT, D, GROUP, NT>())
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
           ref[n][e] = top == -INFINITY ? 0.f : top;
-          alpha[n][e] = exp2f((m[n][e] - ref[n][e]) * qs[n][e]);
+          alpha[e] = exp2f((m[n][e] - ref[n][e]) * qs[n][e]);
           m[n][e] = top;
           high_at[n][e] = top + 6.f / qs[n][e];
-          l[n][e] *= alpha[n][e];
+          l[n][e] *= alpha[e];
         }
 #pragma unroll
-      for (int k = 0; k < G; ++k) {
-        float top = 0.f;
+        for (int k = 0; k < G * KS; ++k)
 #pragma unroll
-        for (int mi = 0; mi < M; ++mi) top = fmaxf(top, fmaxf(fabsf(vs[mi][0][k]), fabsf(vs[mi][1][k])));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-        const float next = fmaxf(vref[k], pow2_below(top));
-        const float beta = vref[k] * pow2_inverse(next);
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int mt = 0; mt < KS; ++mt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[n][k * KS + mt][e] *= alpha[n][e & 1] * beta;
-        vref[k] = next;
+          for (int e = 0; e < 4; ++e) o[n][k][e] *= alpha[e & 1];
       }
     }
+    // The weights' transposes, in upper and lower halves: keys 2t, 2t + 1 (+ 8 r) of column g.
+    float2 p[M][NT][2];
 #pragma unroll
-    for (int mi = 0; mi < M; ++mi) {
+    for (int mi = 0; mi < M; ++mi)
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NT; ++n) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           s[mi][n][e] = exp2_approx((s[mi][n][e] - ref[n][e & 1]) * qs[n][e & 1]);
           l[n][e & 1] += s[mi][n][e];
         }
-      // O += V w, group by group; values 2t, 2t + 1, 2t + 8, 2t + 9
 #pragma unroll
-      for (int k = 0; k < G; ++k) {
-        Raw<VB> vw[4];
+        for (int r = 0; r < 2; ++r) {
+          const uint32_t x = __float_as_uint(s[mi][n][2 * r]), y = __float_as_uint(s[mi][n][2 * r + 1]);
+          const uint32_t up = movmatrix(upper_halves(x, y)), low = movmatrix(lower_halves(x, y));
+          p[mi][n][r] = make_float2(__uint_as_float(lower_halves(low, up)), __uint_as_float(upper_halves(low, up)));
+        }
+      }
+    // O += V w, group by group; keys 2t, 2t + 1, 2t + 8, 2t + 9 of each 16
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          vw[r] = read_raw<VB>(st + St::kV + (16 * mi + 2 * t + (r & 1) + 4 * (r & 2)) * St::kPitch +
-                               k * GROUP * BITS / 8 + g * VB);
-        const float inv = pow2_inverse(vref[k]);
-        uint32_t hi[NT][2], lo[NT][2];
+    for (int k = 0; k < G; ++k) {
+      auto key = [&](int mi, int r) { return 16 * mi + 2 * t + (r & 1) + 4 * (r & 2); };
+      float2 w[NT][M][2];
+      uint32_t tops = 0;  // the largest weight of column g; of both query tiles, the upper halves side by side
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NT; ++n) {
+        float top = 0.f;
+#pragma unroll
+        for (int mi = 0; mi < M; ++mi)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            const float scale = vs[mi][r][k] * inv;
-            const float w0 = s[mi][n][2 * r] * scale, w1 = s[mi][n][2 * r + 1] * scale;
-            // the upper 11 bits, which a half holds, and the rest
-            const float h0 = __uint_as_float(__float_as_uint(w0) & 0xffffe000u);
-            const float h1 = __uint_as_float(__float_as_uint(w1) & 0xffffe000u);
-            hi[n][r] = movmatrix(pack_half2(h0, h1));
-            lo[n][r] = movmatrix(pack_half2(w0 - h0, w1 - h1));
+            w[n][mi][r] = mul2(p[mi][n][r], make_float2(v_scale[key(mi, 2 * r) * SF + k], v_scale[key(mi, 2 * r + 1) * SF + k]));
+            top = fmaxf(fmaxf(top, fabsf(w[n][mi][r].x)), fabsf(w[n][mi][r].y));
           }
+        tops = NT == 2 ? upper_halves(tops, __float_as_uint(top)) : __float_as_uint(top);
+      }
+#pragma unroll
+      for (int i = 1; i < 4; i *= 2) {
+        const uint32_t x = __shfl_xor_sync(0xffffffffu, tops, i);
+        tops = NT == 2 ? __vmaxu2(tops, x) : __float_as_uint(fmaxf(__uint_as_float(tops), __uint_as_float(x)));
+      }
+      if constexpr (NT == 1) tops = __float_as_uint(weight_unit(__uint_as_float(tops)));
+      const uint32_t tops0 = __shfl_sync(0xffffffffu, tops, 8 * t), tops1 = __shfl_sync(0xffffffffu, tops, 8 * t + 4);
+      uint32_t hi[NT][M][2], lo[NT][M][2];
+      float2 unit[NT];  // of columns 2t and 2t + 1
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        auto unit_of = [&](uint32_t x) {
+          return NT == 1 ? __uint_as_float(x) : weight_unit(__uint_as_float(n == 0 ? x << 16 : x));
+        };
+        unit[n] = make_float2(unit_of(tops0), unit_of(tops1));
+        const float2 inv = both(pow2_inverse(unit_of(tops)));
+#pragma unroll
+        for (int mi = 0; mi < M; ++mi)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float2 x = mul2(w[n][mi][r], inv);
+            const __half2 h = __floats2half2_rn(x.x, x.y);
+            const float2 rest = mul2(fma2(__half22float2(h), both(-1.f), x), both(4096.f));
+            hi[n][mi][r] = *reinterpret_cast<const uint32_t*>(&h);
+            lo[n][mi][r] = pack_half2(rest.x, rest.y);
+          }
+      }
+      // 16-key products between two updates of O: both of the unit, or one where a run is 16 bytes and registers are
+      // short (one token over 49920 rows 37 us; with both 38 to 53, as the registers fall)
+      constexpr int KEYS = VB == 16 && NT == 1 ? 1 : M;
+#pragma unroll
+      for (int m0 = 0; m0 < M; m0 += KEYS) {
+        Raw<VB> vw[KEYS][4];
+#pragma unroll
+        for (int mi = 0; mi < KEYS; ++mi)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            vw[mi][r] = read_raw<VB>(st + St::kV + key(m0 + mi, r) * St::kPitch + k * GROUP * BITS / 8 + g * VB);
 #pragma unroll
         for (int mt = 0; mt < KS; ++mt) {
-          uint32_t f[4];
-          two_keys<FMT>(vw[0].w, vw[1].w, mt, f[0], f[1]);
-          two_keys<FMT>(vw[2].w, vw[3].w, mt, f[2], f[3]);
+          float a0[NT][4], a1[NT][4];
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) a0[n][e] = a1[n][e] = 0.f;
+#pragma unroll
+          for (int mi = 0; mi < KEYS; ++mi) {
+            uint32_t f[4];
+            two_keys<FMT>(vw[mi][0].w, vw[mi][1].w, mt, f[0], f[1]);
+            two_keys<FMT>(vw[mi][2].w, vw[mi][3].w, mt, f[2], f[3]);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              mma16816(a0[n], f, hi[n][m0 + mi][0], hi[n][m0 + mi][1]);
+              mma16816(a1[n], f, lo[n][m0 + mi][0], lo[n][m0 + mi][1]);
+            }
+          }
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            mma16816(o[n][k * KS + mt], f, hi[n][0], hi[n][1]);
-            mma16816(o[n][k * KS + mt], f, lo[n][0], lo[n][1]);
+            float* y = o[n][k * KS + mt];
+            const float2 small = mul2(unit[n], both(1.f / 4096.f));
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+              const float2 z = fma2(make_float2(a0[n][e], a0[n][e + 1]), unit[n],
+                                           fma2(make_float2(a1[n][e], a1[n][e + 1]), small, make_float2(y[e], y[e + 1])));
+              y[e] = z.x;
+              y[e + 1] = z.y;
+            }
           }
         }
       }
@@ -561,8 +633,7 @@ __global__ void __launch_bounds__(kAqThreads, (ctas_per_sm<FMT, D, GROUP, NT>())
 #pragma unroll
       for (int k = 0; k < G * KS; ++k) {
         const int d = (k / KS) * GROUP + g * (GROUP / 8) + 2 * (k % KS);
-        const float f = vref[k / KS];
-        *reinterpret_cast<float2*>(dst + d) = make_float2(o[n][k][e] * f * part, o[n][k][2 + e] * f * part);
+        *reinterpret_cast<float2*>(dst + d) = make_float2(o[n][k][e] * part, o[n][k][2 + e] * part);
       }
     }
   __syncthreads();

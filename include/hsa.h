@@ -508,7 +508,9 @@ hsa_status_t hkv_gather_quant(const hkv_quant_t* q, const void* const* page_k, c
  * h / (Hq / H).  Keys are used as stored (rotate them as they are written).  Q:
  * [T, Hq, d] bf16, Hq a multiple of H; out: [T, Hq, d] fp32, or bf16 when out_is_bf16;
  * lse (optional): [T, Hq] fp32.  scale: 0 means 1/sqrt(d).  Scores beyond fp32's range
- * give NaN.  n = 0 gives o = 0 and lse = -inf; a bad page sets HSA_ERR_DEVICE and its rows
+ * give NaN.  Weights are fp32; softmax weight x value scale enters the products with an error
+ * below 2^-22 of its own, or 2^-51 of the largest one of its head, query and group among 32 rows,
+ * and an element of Q with one below 2^-25 of its query's largest.  n = 0 gives o = 0 and lse = -inf; a bad page sets HSA_ERR_DEVICE and its rows
  * are not attended to.  Two results over disjoint rows merge by their lse.  T <= 64; for a whole chunk assemble the cache
  * and use hsa_forward.  T may be 0.  Deterministic.  Workspace:
  * hkv_attn_quant_workspace_size() bytes, its 256-byte header as every workspace's. */
