@@ -33,7 +33,7 @@ EXPORTED = [
     "hsa_sparse_attn_lse", "hsa_fidelity", "hkv_page_block_sums", "hkv_block_means_from_pages",
     "hsa_forward_selected", "hsa_forward_ex", "hkv_gather_project", "hsa_inject_fault",
     "hsa_rope_freqs", "hsa_rope", "hsa_rope_bwd", "hkv_quant_page_size", "hkv_quant_rows", "hkv_gather_quant",
-    "hkv_attn_quant_workspace_size", "hkv_attn_quant",
+    "hkv_attn_quant_workspace_size", "hkv_attn_quant", "hkv_store_write_quant",
 ]
 
 FWD_SELECTED, FWD_HISTORY = 1, 2
@@ -140,6 +140,7 @@ def load_library(path: str = LIB_PATH):
         "hsa_rope_bwd": (I, [RP, P, L, I, I, I, XP, XP, XP, XP, P]),
         "hkv_quant_page_size": (I, [QP, I, I, I, ctypes.POINTER(S), ctypes.POINTER(S)]),
         "hkv_quant_rows": (I, [QP, XP, XP, I, I, I, RP, P, L, P, P, I, I, L, P, P, S, P]),
+        "hkv_store_write_quant": (I, [ctypes.POINTER(StoreDesc), QP, XP, XP, I, I, I, RP, P, L, I, L, P, P, S, P]),
         "hkv_gather_quant": (I, [QP, P, P, I, P, I, I, I, I, RP, P, L, P, P, P, P, S, P]),
         "hkv_attn_quant_workspace_size": (I, [I, I, I, I, I, I, ctypes.POINTER(S)]),
         "hkv_attn_quant": (I, [QP, P, I, I, P, P, I, P, I, I, I, I, P, F, P, I, P, P, S, P]),
@@ -600,22 +601,39 @@ def _tables(where, device, page_k_ptrs, page_v_ptrs, ws):
             _tensor(ws, "ws", where, device, torch.uint8), ws.numel())
 
 
-def hkv_quant_rows(quant: Quant, K, V, page_k_ptrs, page_v_ptrs, P_tok, first_row, ws, first_row_dev=None, rope=None,
-                   pos=None, stream=None):
-    """Quantise rows K, V [T, H, d] (bfloat16, float16 or float32, strided as hsa_rope's) into history rows
-    first_row (+ first_row_dev, a device int64 scalar), ... of the pages; `rope` rotates the keys first."""
-    where, device, dtype = "hkv_quant_rows", K.get_device(), K.dtype
+def _written(where, K, V, first_row_dev, rope, pos):
+    """(device, arguments of the rows K, V and their rotation, first_row_dev's address)."""
+    device, dtype = K.get_device(), K.dtype
     if K.dim() != 3 or dtype not in _DTYPES:
         _refuse(where, f"K is {list(K.shape)} {dtype}: [T, heads, d] bfloat16, float16 or float32 wanted")
     T, _, d = K.shape
     k, v = _rows(K, "K", where, device, dtype, T, d), _rows(V, "V", where, device, dtype, T, d)
-    pk, pv, NP, w, wn = _tables(where, device, page_k_ptrs, page_v_ptrs, ws)
     r, at, step = _positions(rope, pos, where, device, T)
     dev = None
     if first_row_dev is not None:
         dev = _tensor(first_row_dev.view(-1), "first_row_dev", where, device, torch.int64, (1,))
-    _launch(where, device, stream, load_library().hkv_quant_rows, ctypes.byref(quant), k, v, T, d, _DTYPES[dtype], r, at, step,
-            pk, pv, NP, P_tok, first_row, dev, w, wn)
+    return device, (k, v, T, d, _DTYPES[dtype], r, at, step), dev
+
+
+def hkv_quant_rows(quant: Quant, K, V, page_k_ptrs, page_v_ptrs, P_tok, first_row, ws, first_row_dev=None, rope=None,
+                   pos=None, stream=None):
+    """Quantise rows K, V [T, H, d] (bfloat16, float16 or float32, strided as hsa_rope's) into history rows
+    first_row (+ first_row_dev, a device int64 scalar), ... of the pages; `rope` rotates the keys first."""
+    where = "hkv_quant_rows"
+    device, rows, dev = _written(where, K, V, first_row_dev, rope, pos)
+    pk, pv, NP, w, wn = _tables(where, device, page_k_ptrs, page_v_ptrs, ws)
+    _launch(where, device, stream, load_library().hkv_quant_rows, ctypes.byref(quant), *rows, pk, pv, NP, P_tok, first_row, dev, w,
+            wn)
+
+
+def hkv_store_write_quant(desc: StoreDesc, quant: Quant, K, V, P_tok, first_row, ws, first_row_dev=None, rope=None, pos=None,
+                          stream=None):
+    """hkv_quant_rows into the store of `desc`: its host tier, and the slots of pages that are resident."""
+    where = "hkv_store_write_quant"
+    device, rows, dev = _written(where, K, V, first_row_dev, rope, pos)
+    w = _tensor(ws, "ws", where, device, torch.uint8)
+    _launch(where, device, stream, load_library().hkv_store_write_quant, ctypes.byref(desc), ctypes.byref(quant), *rows, P_tok,
+            first_row, dev, w, ws.numel())
 
 
 def hkv_gather_quant(quant: Quant, page_k_ptrs, page_v_ptrs, sel, Kp, P_tok, H, d, Kc, Vc, ws, kbar128=None, rope=None,

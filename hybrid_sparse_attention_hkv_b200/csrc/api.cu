@@ -1123,23 +1123,28 @@ static hsa_status_t quant_args(const char* fn, const hkv_quant_t* q, int P_tok, 
   return HSA_OK;
 }
 
+static long long quant_page_bytes(const hsa::QuantArgs& a) {
+  const long long bytes = a.scale_offset + (long long)a.P_tok * a.H * (a.d / a.group) * (long long)sizeof(float);
+  return (bytes + 1023) / 1024 * 1024;
+}
+
 hsa_status_t hkv_quant_page_size(const hkv_quant_t* q, int P_tok, int H, int d, size_t* page_bytes,
                                  size_t* scale_offset) {
   const char* fn = __func__;
   hsa::QuantArgs a;
   TRY(quant_args(fn, q, P_tok, H, d, &a));
   if (!page_bytes) return fail(HSA_ERR_INVALID_ARG, "%s: page_bytes is NULL", fn);
-  const size_t bytes = (size_t)a.scale_offset + (size_t)P_tok * H * (d / a.group) * sizeof(float);
-  *page_bytes = (bytes + 1023) / 1024 * 1024;
+  *page_bytes = (size_t)quant_page_bytes(a);
   if (scale_offset) *scale_offset = (size_t)a.scale_offset;
   return HSA_OK;
 }
 
-hsa_status_t hkv_quant_rows(const hkv_quant_t* q, const hsa_rows_t* K, const hsa_rows_t* V, int T, int d, int dtype,
-                            const hsa_rope_t* rope, const int32_t* pos, long long pos_stride, void* const* page_k,
-                            void* const* page_v, int NP, int P_tok, long long first_row, const long long* first_row_dev,
-                            void* ws, size_t ws_bytes, hsa_stream_t stream) {
-  const char* fn = __func__;
+// A call that writes rows: to the pages of two tables, or to a store's.
+static hsa_status_t quant_rows_impl(const char* fn, const hkv_quant_t* q, const hsa_rows_t* K, const hsa_rows_t* V, int T,
+                                    int d, int dtype, const hsa_rope_t* rope, const int32_t* pos, long long pos_stride,
+                                    const hkv_store_t* st, void* const* page_k, void* const* page_v, int NP, int P_tok,
+                                    long long first_row, const long long* first_row_dev, void* ws, size_t ws_bytes,
+                                    hsa_stream_t stream) {
   if (T < 0) return fail(HSA_ERR_INVALID_ARG, "%s: T = %d must be >= 0", fn, T);
   if (!dtype_bytes(dtype)) return fail(HSA_ERR_INVALID_ARG, "%s: dtype = %d", fn, dtype);
   hsa::RowsArgs k, v;
@@ -1151,18 +1156,55 @@ hsa_status_t hkv_quant_rows(const hkv_quant_t* q, const hsa_rows_t* K, const hsa
   hsa::RopeArgs r;
   TRY(rope_args(fn, rope, pos, pos_stride, T, d, 1.f, &r));
   if (NP < 1) return fail(HSA_ERR_INVALID_ARG, "%s: NP = %d must be >= 1", fn, NP);
-  TRY(check_pages(fn, page_k, page_v, nullptr, false));
+  hsa::StoreDesc sd;
+  if (st) {
+    TRY(store_desc(fn, st, &sd));
+    const long long held = (long long)st->P_tok * st->H * st->d * 2, bytes = quant_page_bytes(a);
+    if (held != bytes)
+      return fail(HSA_ERR_INVALID_ARG, "%s: the store's pages have %lld bytes, those of %d rows of %d heads %lld", fn, held,
+                  P_tok, k.H, bytes);
+  } else {
+    TRY(check_pages(fn, page_k, page_v, nullptr, false));
+  }
   if (!first_row_dev && (first_row < 0 || first_row > (long long)NP * P_tok - T))
     return fail(HSA_ERR_INVALID_ARG, "%s: rows [%lld, %lld) outside the %d pages of %d", fn, first_row, first_row + T, NP,
                 P_tok);
   if (first_row < -hsa::kQuantMaxRow || first_row > hsa::kQuantMaxRow)
     return fail(HSA_ERR_INVALID_ARG, "%s: first_row = %lld", fn, first_row);
-  OPTIONAL_PTR8(first_row_dev);
+  if ((reinterpret_cast<uintptr_t>(first_row_dev) & 7u) != 0)
+    return fail(HSA_ERR_INVALID_ARG, "%s: first_row_dev is not 8-byte aligned", fn);
   TRY(check_ws(fn, ws, ws_bytes, 256));
   if (T == 0) return HSA_OK;
-  HSA_LAUNCH("quant_rows", hsa::launch_quant_rows(a, r, k, v, T, dtype, page_k, page_v, NP, first_row, first_row_dev,
+  if (!st) {
+    HSA_LAUNCH("quant_rows", hsa::launch_quant_rows(a, r, k, v, T, dtype, page_k, page_v, NP, first_row, first_row_dev,
+                                                    status_of(ws), stream));
+    return HSA_OK;
+  }
+  // Twice: into the host tier, and into the slots of the pages that are in one (rows of the others go nowhere, with no
+  // status set).
+  const hsa::StoreTables t = hsa::store_write_tables(sd);
+  HSA_LAUNCH("quant_rows", hsa::launch_quant_rows(a, r, k, v, T, dtype, t.host_k, t.host_v, NP, first_row, first_row_dev,
                                                   status_of(ws), stream));
+  HSA_LAUNCH("quant_rows_slots", hsa::launch_quant_rows(a, r, k, v, T, dtype, t.slot_k, t.slot_v, NP, first_row,
+                                                        first_row_dev, nullptr, stream));
   return HSA_OK;
+}
+
+hsa_status_t hkv_quant_rows(const hkv_quant_t* q, const hsa_rows_t* K, const hsa_rows_t* V, int T, int d, int dtype,
+                            const hsa_rope_t* rope, const int32_t* pos, long long pos_stride, void* const* page_k,
+                            void* const* page_v, int NP, int P_tok, long long first_row, const long long* first_row_dev,
+                            void* ws, size_t ws_bytes, hsa_stream_t stream) {
+  return quant_rows_impl(__func__, q, K, V, T, d, dtype, rope, pos, pos_stride, nullptr, page_k, page_v, NP, P_tok, first_row,
+                         first_row_dev, ws, ws_bytes, stream);
+}
+
+hsa_status_t hkv_store_write_quant(const hkv_store_t* st, const hkv_quant_t* q, const hsa_rows_t* K, const hsa_rows_t* V, int T,
+                                   int d, int dtype, const hsa_rope_t* rope, const int32_t* pos, long long pos_stride,
+                                   int P_tok, long long first_row, const long long* first_row_dev, void* ws,
+                                   size_t ws_bytes, hsa_stream_t stream) {
+  if (!st) return fail(HSA_ERR_INVALID_ARG, "%s: store is NULL", __func__);
+  return quant_rows_impl(__func__, q, K, V, T, d, dtype, rope, pos, pos_stride, st, nullptr, nullptr, st->NP, P_tok, first_row,
+                         first_row_dev, ws, ws_bytes, stream);
 }
 
 hsa_status_t hkv_gather_quant(const hkv_quant_t* q, const void* const* page_k, const void* const* page_v, int NP,

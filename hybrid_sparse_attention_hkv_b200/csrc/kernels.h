@@ -68,6 +68,14 @@ struct StoreDesc {
 };
 size_t store_state_bytes(int NP, int S);
 size_t store_table_offset(int NP, int kv);  // byte offset of the K (kv = 0) or V page table
+// The tables through which rows are written: every page's address in the host tier, and in its slot (NULL: in none).
+struct StoreTables {
+  void* const* host_k;
+  void* const* host_v;
+  void* const* slot_k;
+  void* const* slot_v;
+};
+StoreTables store_write_tables(const StoreDesc& st);
 cudaError_t launch_store_init(const StoreDesc& st, cudaStream_t s);
 cudaError_t launch_store_fetch(const StoreDesc& st, const int32_t* sel, int Kp, int* status, cudaStream_t s);
 cudaError_t launch_store_prefetch(const StoreDesc& st, const float* scores, const int32_t* protect, int n_protect,

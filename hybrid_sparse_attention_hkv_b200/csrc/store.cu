@@ -31,6 +31,8 @@
 //   page_of_slot     int32 [S]    -1 = free
 //   stamp            int32 [S]    tick of the last use
 //   copy_list        int2  [S]    (page, slot) pairs to copy after a fetch / prefetch
+//   host_k, host_v   uint64 [NP]  addresses of the host copies
+//   in_slot_k, _v    uint64 [NP]  addresses of the slots' copies, 0 = not resident
 #include "common.cuh"
 #include "kernels.h"
 
@@ -40,7 +42,7 @@ namespace {
 inline size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct StoreLayout {
-  size_t table_k, table_v, slot_of_page, page_of_slot, stamp, copy_list, total;
+  size_t table_k, table_v, slot_of_page, page_of_slot, stamp, copy_list, host_k, host_v, in_slot_k, in_slot_v, total;
 };
 
 StoreLayout store_layout(int NP, int S) {
@@ -52,6 +54,10 @@ StoreLayout store_layout(int NP, int S) {
   L.page_of_slot = off; off += al256((size_t)S * 4);
   L.stamp = off; off += al256((size_t)S * 4);
   L.copy_list = off; off += al256((size_t)S * 8);
+  L.host_k = off; off += al256((size_t)NP * 8);
+  L.host_v = off; off += al256((size_t)NP * 8);
+  L.in_slot_k = off; off += al256((size_t)NP * 8);
+  L.in_slot_v = off; off += al256((size_t)NP * 8);
   L.total = off;
   return L;
 }
@@ -64,6 +70,10 @@ struct StoreView {
   int* page_of_slot;
   int* stamp;
   int2* copy_list;
+  unsigned long long* host_k;
+  unsigned long long* host_v;
+  unsigned long long* in_slot_k;
+  unsigned long long* in_slot_v;
 };
 
 StoreView view_of(const StoreDesc& st) {
@@ -76,6 +86,10 @@ StoreView view_of(const StoreDesc& st) {
   v.page_of_slot = reinterpret_cast<int*>(st.state + L.page_of_slot);
   v.stamp = reinterpret_cast<int*>(st.state + L.stamp);
   v.copy_list = reinterpret_cast<int2*>(st.state + L.copy_list);
+  v.host_k = reinterpret_cast<unsigned long long*>(st.state + L.host_k);
+  v.host_v = reinterpret_cast<unsigned long long*>(st.state + L.host_v);
+  v.in_slot_k = reinterpret_cast<unsigned long long*>(st.state + L.in_slot_k);
+  v.in_slot_v = reinterpret_cast<unsigned long long*>(st.state + L.in_slot_v);
   return v;
 }
 
@@ -91,8 +105,9 @@ __global__ void store_init_kernel(const StoreDesc st, const StoreView v) {
     v.hdr[1] = 0;
   }
   if (i < st.NP) {
-    v.table_k[i] = page_addr(st.host_k, i, pe);
-    v.table_v[i] = page_addr(st.host_v, i, pe);
+    v.table_k[i] = v.host_k[i] = page_addr(st.host_k, i, pe);
+    v.table_v[i] = v.host_v[i] = page_addr(st.host_v, i, pe);
+    v.in_slot_k[i] = v.in_slot_v[i] = 0;
     v.slot_of_page[i] = -1;
   }
   if (i < st.S) {
@@ -107,14 +122,15 @@ __device__ void assign_slot(const StoreDesc& st, const StoreView& v, int p, int 
   const int q = v.page_of_slot[slot];
   if (q >= 0) {  // demote: the gather reads q from the host tier again
     v.slot_of_page[q] = -1;
-    v.table_k[q] = page_addr(st.host_k, q, pe);
-    v.table_v[q] = page_addr(st.host_v, q, pe);
+    v.table_k[q] = v.host_k[q];
+    v.table_v[q] = v.host_v[q];
+    v.in_slot_k[q] = v.in_slot_v[q] = 0;
   }
   v.page_of_slot[slot] = p;
   v.slot_of_page[p] = slot;
   v.stamp[slot] = tick;
-  v.table_k[p] = page_addr(st.slot_k, slot, pe);
-  v.table_v[p] = page_addr(st.slot_v, slot, pe);
+  v.table_k[p] = v.in_slot_k[p] = page_addr(st.slot_k, slot, pe);
+  v.table_v[p] = v.in_slot_v[p] = page_addr(st.slot_v, slot, pe);
   v.copy_list[n_copy++] = make_int2(p, slot);
 }
 
@@ -259,6 +275,12 @@ size_t store_state_bytes(int NP, int S) { return store_layout(NP, S).total; }
 size_t store_table_offset(int NP, int kv) {
   const StoreLayout L = store_layout(NP, 1);
   return kv ? L.table_v : L.table_k;
+}
+
+StoreTables store_write_tables(const StoreDesc& st) {
+  const StoreView v = view_of(st);
+  auto table = [](unsigned long long* p) { return reinterpret_cast<void* const*>(p); };
+  return {table(v.host_k), table(v.host_v), table(v.in_slot_k), table(v.in_slot_v)};
 }
 
 cudaError_t launch_store_init(const StoreDesc& st, cudaStream_t s) {

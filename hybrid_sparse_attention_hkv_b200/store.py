@@ -12,7 +12,7 @@ import ctypes
 import torch
 
 from . import (Quant, StoreDesc, _check, _p, _refuse, _stream, hkv_attn_quant, hkv_gather_quant, hkv_page_summary,
-               hkv_quant_page_size, hkv_quant_rows, load_library)
+               hkv_quant_page_size, hkv_store_write_quant, load_library)
 
 
 class MappedHostMemory:
@@ -98,24 +98,23 @@ class PageStore:
 class QuantPageStore(PageStore):
     """A page store whose pages are quantised: half or a quarter of the host tier, of the HBM slots and of the host link's
     traffic of bf16 pages.  The residency calls (fetch, prefetch, residency) are PageStore's: to them a page is a block of
-    bytes, passed as page_bytes / 1024 rows of 4 x 128 bf16 elements.  Rows are written to the host tier; a page is fetched
-    once its rows are written (a slot keeps the copy it was given)."""
+    bytes, passed as page_bytes / 1024 rows of 4 x 128 bf16 elements.  Rows are written to the host tier and to the slots of
+    pages that are resident: a page may be fetched before all its rows are written."""
 
     def __init__(self, quant: Quant, NP: int, S: int, P_tok: int, H: int, d: int, host=None, stream=None):
         self.quant, self.rows, self.heads, self.head_dim = quant, P_tok, H, d
         self.page_bytes, self.scale_offset = hkv_quant_page_size(quant, P_tok, H, d)
         super().__init__(NP, S, self.page_bytes // 1024, 4, 128, host, stream)
-        at = torch.arange(NP, dtype=torch.int64) * self.page_bytes
-        self.host_tables = tuple((at + h.dev_ptr).to(self.slot_k.device) for h in self.host)
 
     def _open(self, call):
         if self.host is None:
             _refuse(f"QuantPageStore.{call}", "the store is closed: its host tier is gone")
 
     def write(self, K, V, first_row: int, ws, first_row_dev=None, rope=None, pos=None, stream=None):
-        """Append rows K, V [T, H, d] at history row first_row (+ first_row_dev): hkv_quant_rows into the host tier."""
+        """Append rows K, V [T, H, d] at history row first_row (+ first_row_dev), in stream order with the store's other
+        calls: hkv_quant_rows into the host tier, and into the slots of resident pages."""
         self._open("write")
-        hkv_quant_rows(self.quant, K, V, *self.host_tables, self.rows, first_row, ws, first_row_dev, rope, pos, stream)
+        hkv_store_write_quant(self.desc, self.quant, K, V, self.rows, first_row, ws, first_row_dev, rope, pos, stream)
 
     def seal(self, page: int, K_rows, V_rows, kbar_out, ws, rope=None, pos=None, stream=None):
         """Write the rows of page `page` and its summary kbar_out (the mean of K_rows, bf16, before any rotation)."""

@@ -461,7 +461,7 @@ hsa_status_t hsa_rope_bwd(const hsa_rope_t* rope, const int32_t* pos, long long 
  *                        the codes rounded up to 256 bytes
  * The size is a multiple of 1024, so an hkv_store_t of P_tok = page_bytes / 1024, H = 4,
  * d = 128 keeps such pages in its two tiers: every hkv_store_* call but
- * hkv_store_seal works on it as on bf16 pages (hkv_quant_rows writes the host tier). */
+ * hkv_store_seal works on it as on bf16 pages (hkv_store_write_quant writes its rows). */
 #define HKV_QUANT_E4M3 0
 #define HKV_QUANT_INT8 1
 #define HKV_QUANT_INT4 2
@@ -487,6 +487,16 @@ hsa_status_t hkv_quant_rows(const hkv_quant_t* q, const hsa_rows_t* K, const hsa
                             const hsa_rope_t* rope, const int32_t* pos, long long pos_stride, void* const* page_k,
                             void* const* page_v, int NP, int P_tok, long long first_row, const long long* first_row_dev,
                             void* ws, size_t ws_bytes, hsa_stream_t stream);
+
+/* hkv_quant_rows into a store of quantised pages: the rows go to the host tier and, of pages
+ * that are in HBM slots when the call runs, to their slots as well, so that what reads through
+ * the store's tables afterwards sees them (an open page may be fetched while it fills).
+ * Residency stays as it is.  The store's NP pages are those of hkv_quant_page_size()
+ * bytes for P_tok rows of K->H heads.  Ordered with the store's other calls. */
+hsa_status_t hkv_store_write_quant(const hkv_store_t* st, const hkv_quant_t* q, const hsa_rows_t* K, const hsa_rows_t* V, int T,
+                                   int d, int dtype, const hsa_rope_t* rope, const int32_t* pos, long long pos_stride,
+                                   int P_tok, long long first_row, const long long* first_row_dev, void* ws,
+                                   size_t ws_bytes, hsa_stream_t stream);
 
 /* Active-cache assembly from quantised pages, as hkv_gather: for i < Kp,
  *   Vc[i*P_tok + t] = bf16(page_v[sel[i]][t]),  Kc[i*P_tok + t] = bf16(rotated page_k[sel[i]][t])
