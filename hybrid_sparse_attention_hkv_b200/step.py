@@ -102,6 +102,8 @@ class HkvHsaStep:
         dtype as self.out) when given, else to self.out."""
         dst = self.out if out is None else out
         cand = None
+        if self.store is not None:
+            self.store.check_open("fetch")  # the tables that the step reads lead into its host tier
         if e_cur is not None:
             hkv_select_prompt(e_cur, e_seg, seg_begin, self.seg, self.cand_range)
             cand = self.cand_range
@@ -134,6 +136,8 @@ class HkvHsaStep:
         """Once per chunk: retrieval (prompt-level, page-level) with the chunk's queries,
         the gather of the active cache, and the cached KV's Linformer products."""
         cand = None
+        if self.store is not None:
+            self.store.check_open("fetch")  # the tables that the step reads lead into its host tier
         if e_cur is not None:
             hkv_select_prompt(e_cur, e_seg, seg_begin, self.seg, self.cand_range)
             cand = self.cand_range

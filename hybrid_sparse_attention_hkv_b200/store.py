@@ -60,22 +60,31 @@ class PageStore:
         _check(lib.hkv_store_tables(ctypes.byref(self.desc), ctypes.byref(tk), ctypes.byref(tv)), "hkv_store_tables")
         self.table_k, self.table_v = tk.value, tv.value
 
+    def check_open(self, call):
+        """Refuse what would launch kernels over the host tier of a closed store."""
+        if self.host is None:
+            _refuse(f"{type(self).__name__}.{call}", "the store is closed: its host tier is gone")
+
     def page_tables(self):
-        """(K, V) device page tables as int64 tensor views (for hkv_gather)."""
+        """(K, V) device page tables as int64 tensor views (for hkv_gather).  Not to be read once the store is closed."""
+        self.check_open("page_tables")
         n = self.NP
         off_k = self.table_k - self.state.data_ptr()
         off_v = self.table_v - self.state.data_ptr()
         return (self.state[off_k:off_k + 8 * n].view(torch.int64), self.state[off_v:off_v + 8 * n].view(torch.int64))
 
     def seal(self, page: int, K_rows, V_rows, kbar_out, ws, stream=None):
+        self.check_open("seal")
         _check(load_library().hkv_store_seal(ctypes.byref(self.desc), page, _p(K_rows), _p(V_rows), _p(kbar_out),
                                              _p(ws), ws.numel(), _stream(stream)), "hkv_store_seal")
 
     def fetch(self, sel, ws, stream=None):
+        self.check_open("fetch")
         _check(load_library().hkv_store_fetch(ctypes.byref(self.desc), _p(sel), sel.numel(), _p(ws), ws.numel(),
                                               _stream(stream)), "hkv_store_fetch")
 
     def prefetch(self, scores, protect, m: int, ws, stream=None):
+        self.check_open("prefetch")
         n = 0 if protect is None else protect.numel()
         _check(load_library().hkv_store_prefetch(ctypes.byref(self.desc), _p(scores), _p(protect), n, m, _p(ws),
                                                  ws.numel(), _stream(stream)), "hkv_store_prefetch")
@@ -89,7 +98,9 @@ class PageStore:
         return sp, ps
 
     def close(self):
-        if self._own:
+        """Free the host tier where the store owns it (after the kernels that may be reading it); once."""
+        if self.host is not None and self._own:
+            torch.cuda.synchronize(self.slot_k.device)
             for h in self.host:
                 h.close()
         self.host = None
@@ -106,14 +117,10 @@ class QuantPageStore(PageStore):
         self.page_bytes, self.scale_offset = hkv_quant_page_size(quant, P_tok, H, d)
         super().__init__(NP, S, self.page_bytes // 1024, 4, 128, host, stream)
 
-    def _open(self, call):
-        if self.host is None:
-            _refuse(f"QuantPageStore.{call}", "the store is closed: its host tier is gone")
-
     def write(self, K, V, first_row: int, ws, first_row_dev=None, rope=None, pos=None, stream=None):
         """Append rows K, V [T, H, d] at history row first_row (+ first_row_dev), in stream order with the store's other
         calls: hkv_quant_rows into the host tier, and into the slots of resident pages."""
-        self._open("write")
+        self.check_open("write")
         hkv_store_write_quant(self.desc, self.quant, K, V, self.rows, first_row, ws, first_row_dev, rope, pos, stream)
 
     def seal(self, page: int, K_rows, V_rows, kbar_out, ws, rope=None, pos=None, stream=None):
@@ -128,12 +135,12 @@ class QuantPageStore(PageStore):
 
     def gather(self, sel, Kc, Vc, ws, kbar128=None, rope=None, pos=None, stream=None):
         """hkv_gather_quant of the pages `sel` (int32 device tensor), from their slots or the host tier."""
-        self._open("gather")
+        self.check_open("gather")
         hkv_gather_quant(self.quant, *self.page_tables(), sel, sel.numel(), self.rows, self.heads, self.head_dim, Kc, Vc, ws,
                          kbar128, rope, pos, stream)
 
     def attend(self, Q, sel, out, lse, ws, n_rows=None, scale=0.0, stream=None):
         """hkv_attn_quant of a few queries over the pages `sel`."""
-        self._open("attend")
+        self.check_open("attend")
         hkv_attn_quant(self.quant, Q, *self.page_tables(), sel, sel.numel(), self.rows, self.heads, out, lse, ws, n_rows, scale,
                        stream)

@@ -70,3 +70,70 @@ def test_binding_of_the_store_write_checks_its_tensors(lib):
         with pytest.raises(hsa.HsaError) as e:
             bad()
         assert e.value.code == 1
+
+
+class FreedHost:
+    """A host tier that can be freed once."""
+
+    def __init__(self):
+        self.dev_ptr, self.freed = A, 0
+
+    def close(self):
+        self.freed += 1
+
+
+def a_store(kind, own=False):
+    """A store object without its device memory."""
+    s = kind.__new__(kind)
+    s._own, s.host = own, (FreedHost(), FreedHost())
+    s.desc, s.NP, s.S, s.table_k, s.table_v = store(), 4, 2, 0, 0
+    s.quant, s.rows, s.heads, s.head_dim = hsa.make_quant(0, 64), 8, 2, 64
+    s.state = s.slot_k = torch.zeros(256, dtype=torch.uint8)
+    return s
+
+
+@pytest.mark.parametrize("quantised", [False, True])
+def test_a_closed_store_neither_copies_nor_gives_its_tables(lib, quantised):
+    """Their kernels and readers would go to host memory that is gone."""
+    from hybrid_sparse_attention_hkv_b200.store import PageStore, QuantPageStore
+    s = a_store(QuantPageStore if quantised else PageStore)
+    s.close()
+    sel, ws, x = torch.zeros(1, dtype=torch.int32), torch.zeros(256, dtype=torch.uint8), torch.zeros(8, 2, 64, dtype=torch.bfloat16)
+    for call in (lambda: s.fetch(sel, ws), lambda: s.prefetch(torch.zeros(4), None, 1, ws), lambda: s.page_tables(),
+                 lambda: s.seal(0, x, x, torch.zeros(2, 64), ws)):
+        with hsa.injected_fault(hsa.FAULT_LAUNCH):  # nothing is launched whatever the call does
+            with pytest.raises(hsa.HsaError, match="closed"):
+                call()
+
+
+def test_a_store_is_closed_once(monkeypatch):
+    from hybrid_sparse_attention_hkv_b200.store import QuantPageStore
+    waited = []
+    monkeypatch.setattr(torch.cuda, "synchronize", lambda device=None: waited.append(device))
+    s = a_store(QuantPageStore, own=True)
+    held = s.host
+    s.close()
+    s.close()
+    assert [h.freed for h in held] == [1, 1]
+    assert len(waited) == 1  # kernels on their way through the host tier end before it goes
+
+
+@pytest.mark.parametrize("quantised", [False, True])
+def test_a_step_over_a_closed_store_launches_nothing(monkeypatch, quantised):
+    """The step kept the store's tables: it looks before its first launch."""
+    from hybrid_sparse_attention_hkv_b200 import step as module
+    from hybrid_sparse_attention_hkv_b200.store import PageStore, QuantPageStore
+    s = a_store(QuantPageStore if quantised else PageStore)
+    st = module.HkvHsaStep.__new__(module.HkvHsaStep)
+    st.store, st.out, st.rope = s, None, None
+    s.close()
+
+    def launched(*a, **k):
+        raise AssertionError("launched")
+    for name in ("hkv_select_pages", "hkv_select_prompt", "hkv_gather", "hkv_gather_quant", "hkv_block_means_from_pages"):
+        monkeypatch.setattr(module, name, launched)
+    st.kbar_pages = st.Kp = st.sel = st.ws = st.scores = st.seg = st.cand_range = None
+    for call in (lambda: st(None, None, None, None, None, None, None), lambda: st.prepare_chunk(None, None, None),
+                 lambda: st(None, None, None, None, None, None, None, e_cur=0), lambda: st.prepare_chunk(None, None, None, e_cur=0)):
+        with pytest.raises(hsa.HsaError, match="closed"):
+            call()
