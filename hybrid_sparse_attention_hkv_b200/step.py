@@ -9,6 +9,8 @@ arithmetic happens in the library's kernels.
 """
 from __future__ import annotations
 
+import warnings
+
 import torch
 
 from . import (FWD_SELECTED, SelectionBuffers, hkv_block_means_from_pages, hkv_gather, hkv_gather_quant,
@@ -36,7 +38,8 @@ class HkvHsaStep:
         rope, pos (make_rope; int32 [n_axes, Kp * P_tok]): their keys are rotated as they
         are read, to their places in the active cache; Q and Kq come rotated (hsa_rope),
         and the page retrieval, whose summaries are of the keys before their rotation,
-        takes the queries before theirs (`q_pages` of the calls; None: Q)."""
+        takes the queries before theirs: pass them as `q_pages` (a call without them retrieves
+        by the rotated Q, which is rarely what is wanted, and warns)."""
         held = getattr(store, "quant", None)
         if store is not None and (held is None) != (quant is None):
             raise ValueError(f"the store's pages are {'bf16' if held is None else 'quantised'}, the step's are "
@@ -82,6 +85,13 @@ class HkvHsaStep:
             if self.early:
                 hkv_page_block_sums(pages_k[p], self.sums64[p])
 
+    def _page_queries(self, Q, q_pages):
+        """The queries that the pages are retrieved by."""
+        if q_pages is None and self.rope is not None:
+            warnings.warn("pages are retrieved by the rotated queries against summaries of the keys before their rotation: pass "
+                          "the queries before theirs as q_pages (q_pages=Q where that is meant)", stacklevel=3)
+        return Q if q_pages is None else q_pages
+
     def _retrieve(self, Q, cand):
         """Page-level retrieval into self.sel (self.scores: the page scores)."""
         hkv_select_pages(self.kbar_pages, Q, self.Kp, self.sel, self.ws, self.scores, cand)
@@ -107,7 +117,7 @@ class HkvHsaStep:
         if e_cur is not None:
             hkv_select_prompt(e_cur, e_seg, seg_begin, self.seg, self.cand_range)
             cand = self.cand_range
-        self._retrieve(Q if q_pages is None else q_pages, cand)
+        self._retrieve(self._page_queries(Q, q_pages), cand)
         if self.store is not None:
             self.store.fetch(self.sel, self.ws)
         if not self.early:
@@ -141,7 +151,7 @@ class HkvHsaStep:
         if e_cur is not None:
             hkv_select_prompt(e_cur, e_seg, seg_begin, self.seg, self.cand_range)
             cand = self.cand_range
-        self._retrieve(Q if q_pages is None else q_pages, cand)
+        self._retrieve(self._page_queries(Q, q_pages), cand)
         if self.store is not None:
             self.store.fetch(self.sel, self.ws)
         self._gather()
