@@ -116,6 +116,7 @@ class QuantPageStore(PageStore):
         self.quant, self.rows, self.heads, self.head_dim = quant, P_tok, H, d
         self.page_bytes, self.scale_offset = hkv_quant_page_size(quant, P_tok, H, d)
         super().__init__(NP, S, self.page_bytes // 1024, 4, 128, host, stream)
+        self.P_tok, self.H, self.d = P_tok, H, d  # of the pages; `desc` has the block's
 
     def write(self, K, V, first_row: int, ws, first_row_dev=None, rope=None, pos=None, stream=None):
         """Append rows K, V [T, H, d] at history row first_row (+ first_row_dev), in stream order with the store's other

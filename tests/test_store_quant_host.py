@@ -137,3 +137,18 @@ def test_a_step_over_a_closed_store_launches_nothing(monkeypatch, quantised):
                  lambda: st(None, None, None, None, None, None, None, e_cur=0), lambda: st.prepare_chunk(None, None, None, e_cur=0)):
         with pytest.raises(hsa.HsaError, match="closed"):
             call()
+
+
+def test_a_quantised_store_has_the_shape_of_its_pages(lib, monkeypatch):
+    """P_tok, H and d are the rows', heads' and columns' of its pages, as a PageStore's; the block of bytes that its residency
+    calls move is the descriptor's."""
+    from hybrid_sparse_attention_hkv_b200 import store as module
+
+    def no_memory(self, NP, S, P_tok, H, d, host=None, stream=None):
+        self.NP, self.S, self.P_tok, self.H, self.d, self.host = NP, S, P_tok, H, d, (FreedHost(), FreedHost())
+        self.slot_k = torch.zeros(1)
+        self.desc = store(NP, S, P_tok, H, d)
+    monkeypatch.setattr(module.PageStore, "__init__", no_memory)
+    s = module.QuantPageStore(hsa.make_quant(1, 32), 5, 2, 200, 3, 128)
+    assert (s.NP, s.S, s.P_tok, s.H, s.d) == (5, 2, 200, 3, 128) == (s.NP, s.S, s.rows, s.heads, s.head_dim)
+    assert s.desc.P_tok * s.desc.H * s.desc.d * 2 == s.page_bytes == hsa.hkv_quant_page_size(s.quant, 200, 3, 128)[0]
