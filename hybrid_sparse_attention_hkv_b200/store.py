@@ -122,6 +122,8 @@ class QuantPageStore(PageStore):
         """Append rows K, V [T, H, d] at history row first_row (+ first_row_dev), in stream order with the store's other
         calls: hkv_quant_rows into the host tier, and into the slots of resident pages."""
         self.check_open("write")
+        if K.get_device() != self.slot_k.get_device():
+            _refuse("QuantPageStore.write", f"K is on {K.device}, the store on {self.slot_k.device}")
         hkv_store_write_quant(self.desc, self.quant, K, V, self.rows, first_row, ws, first_row_dev, rope, pos, stream)
 
     def seal(self, page: int, K_rows, V_rows, kbar_out, ws, rope=None, pos=None, stream=None):

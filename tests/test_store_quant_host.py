@@ -152,3 +152,20 @@ def test_a_quantised_store_has_the_shape_of_its_pages(lib, monkeypatch):
     s = module.QuantPageStore(hsa.make_quant(1, 32), 5, 2, 200, 3, 128)
     assert (s.NP, s.S, s.P_tok, s.H, s.d) == (5, 2, 200, 3, 128) == (s.NP, s.S, s.rows, s.heads, s.head_dim)
     assert s.desc.P_tok * s.desc.H * s.desc.d * 2 == s.page_bytes == hsa.hkv_quant_page_size(s.quant, 200, 3, 128)[0]
+
+
+def test_rows_on_another_device_than_the_store_are_refused(lib):
+    """Its tables are in the memory of its own device."""
+    from hybrid_sparse_attention_hkv_b200.store import QuantPageStore
+
+    class OnAnother:
+        device = "cuda:1"
+
+        def get_device(self):
+            return 1
+    s = a_store(QuantPageStore)
+    x, ws = torch.zeros(8, 2, 64, dtype=torch.bfloat16), torch.zeros(256, dtype=torch.uint8)
+    s.slot_k = OnAnother()
+    for call in (lambda: s.write(x, x, 0, ws), lambda: s.seal(0, x, x, torch.zeros(2, 64), ws)):
+        with pytest.raises(hsa.HsaError, match="K is on cpu, the store on cuda:1"):
+            call()
