@@ -59,7 +59,8 @@ constexpr int kAqRows = 32;    // keys of a warp's unit
 constexpr int kAqStages = 2;   // tiles of the ring
 constexpr int kAqMostCtas = 4;
 
-// CTAs on an SM, with up to 8 (NT = 1) or 16 queries to a tile: as many as registers and the ring allow.
+// CTAs on an SM, with up to 8 (NT = 1) or 16 queries to a tile: as many as registers and the ring allow (56 of the 90
+// instances spill, up to 80 bytes).
 template <int FMT, int D, int GROUP, int NT>
 constexpr int ctas_per_sm() {
   if (NT == 2) return D == 64 ? 3 : 2;
@@ -90,6 +91,8 @@ __device__ __forceinline__ uint32_t hsub2_u(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&d);
 }
 
+// Integers become halves through the mantissa of 1024, a published conversion (Kim, Henry, Fahim and Awadalla, "Who Says
+// Elephants Can't Run", 2022, for unsigned ones), which costs a mask or a byte permute and a subtraction for two.
 // The low two nibbles of each half of w as halves: p0 the lowest of both, p1 the next.  Flipping
 // a nibble's sign bit gives n + 8, which becomes the low bits of 1024 + (n + 8), or, left where
 // it is, of 1024 + 16 (n + 8).

@@ -25,17 +25,6 @@ struct Codes8 {
 };
 
 template <int FMT>
-__device__ __forceinline__ Codes8<FMT> load_codes(const void* p) {
-  Codes8<FMT> c;
-  if constexpr (FMT == HKV_QUANT_INT4) {
-    asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(c.w[0]) : "l"(p));
-  } else {
-    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(c.w[0]), "=r"(c.w[1]) : "l"(p));
-  }
-  return c;
-}
-
-template <int FMT>
 __device__ __forceinline__ void store_codes(void* p, const Codes8<FMT>& c) {
   if constexpr (FMT == HKV_QUANT_INT4) *static_cast<uint32_t*>(p) = c.w[0];
   else *static_cast<uint2*>(p) = make_uint2(c.w[0], c.w[1]);

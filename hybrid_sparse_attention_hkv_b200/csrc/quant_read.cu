@@ -22,7 +22,7 @@ namespace {
 // 40).  The cos and sin of 32 rows at a time are computed
 // into shared memory (all heads of the slab use them).  The block means are summed a thread's
 // rows first, then phase by phase in order (deterministic).
-constexpr int kReadCtas = 3;  // on an SM
+constexpr int kReadCtas = 3;  // on an SM (8 of the 36 instances spill, up to 16 bytes)
 constexpr int kReadRing = 4;
 constexpr int kReadThreads = 320;
 constexpr int kReadRows = 16;   // of a CTA, or more:
@@ -236,7 +236,9 @@ __global__ void __launch_bounds__(kReadThreads, ROPE == kRopeHalf && POOL ? 2 : 
 
 // The shares of CTAs of 128 rows (for the block means), or of about 16, in eight rounds or more,
 // fewer where a short cache leaves SMs idle.  Slabs are as wide as they can be, or narrower (and
-// so more rows at once) where a short cache leaves SMs idle all the same.
+// so more rows at once) where a short cache leaves SMs idle all the same.  Whole waves are not looked
+// at: 4689 rows of 12 heads make 626 CTAs for 444 places, a second wave that is mostly empty, which is
+// part of why they take 12 us where their bytes take 6.
 template <int J>
 ReadArgs::Part read_part(const ReadArgs& a, bool pool) {
   ReadArgs::Part p;

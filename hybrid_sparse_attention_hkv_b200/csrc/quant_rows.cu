@@ -19,7 +19,7 @@ namespace {
 // ahead in registers, 97 with K and V of a head in one thread and nothing ahead); the tokens'
 // places and their cos and sin are computed while the first ones are.
 constexpr int kRowsThreads = 320;
-constexpr int kRowsCtas = 4;   // on an SM
+constexpr int kRowsCtas = 4;   // on an SM (48 registers: 29 of the 135 instances spill, up to 28 bytes)
 constexpr int kRowsRing = 3;
 constexpr int kRowsRounds = 8;
 constexpr int kRowsMaxRows = 64;  // tokens of a CTA (32 KB of cos and sin at d = 128)
@@ -77,7 +77,8 @@ __device__ __forceinline__ void group_amax(const RopeArgs& r, const ChunkPair& c
   }
 }
 
-// What a group is multiplied with (NaN where it is not finite) and its scale.
+// What a group is multiplied with (0 where it is stored as zeros, or is not finite) and its scale (NaN where it is not
+// finite).
 template <int FMT>
 __device__ __forceinline__ void group_scale(float amax, float& inv, float& scale) {
   const bool kept = amax >= kQuantTiny && amax < INFINITY;
