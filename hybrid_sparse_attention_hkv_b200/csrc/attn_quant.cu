@@ -38,14 +38,14 @@
 // 49920 rows of 40 heads).  Tiles are on their way to a ring in shared memory while one is
 // worked on; small CTAs, three to an SM, drift apart and keep the loads going where one of 8 or
 // 12 warps stops at its barrier (before the weights took their present form 329 us for 199680 rows
-// of 40 heads against 395 to 425; 380 with it, 0.85 of the copy rate).  The splits are joined by a
+// of 40 heads against 395 to 425; 334 with it, 0.96 of the copy rate).  The splits are joined by a
 // second kernel in order (deterministic).  A tile never straddles pages; what lies behind a page's
 // or the cache's end is fetched as zeros and gets no weight.
 //
 // Short caches are bound by their latency: two launches, the way from the row count to the page
 // table to the rows, and the join cost 9 us together.  4-bit codes, and groups of 32 columns, are
 // bound by instructions: turning codes into operands, and scaling and splitting the weights for each
-// group (49920 rows of 12 heads of 128 columns in 8 bits, 4 bits, 8 bits in groups of 32: 37, 37 and 49 us).
+// group (49920 rows of 12 heads of 128 columns in 8 bits, 4 bits, 8 bits in groups of 32: 37, 36 and 50 us).
 #include "common.cuh"
 #include "kernels.h"
 #include "quant.cuh"

@@ -77,8 +77,8 @@ cudaError_t launch(const RopeArgs& r, int tokens, const RowsArgs& qi, const Rows
   // Tokens of a CTA: where there are CTAs enough for every SM, of those that its threads get
   // through in kRopeRounds rounds the number that leaves the fewest of them idle in the last
   // one.  Its heads are shared out as well while that leaves SMs idle.  Whole waves of CTAs are not looked at: 4099 fp32
-  // tokens of 15 heads of 64 make 1025 CTAs for 888 places (9.9 us, 4.8 for the bytes), 4680 tokens of 24 heads 1170
-  // (10.9 us, 8.8 for the bytes).
+  // tokens of 15 heads of 64 make 1025 CTAs for 888 places (9.7 us, 4.8 for the bytes), 4680 tokens of 24 heads 1170
+  // (10.7 us, 8.8 for the bytes).
   int rows = 1, best = 0;
   const int most = tokens / (148 * kRopeCtas);
   for (int n = 1; n == 1 || (n <= kRopeMaxRows && n <= most); ++n) {

@@ -395,7 +395,7 @@ typedef struct {
   int n_axes;              /* position axes, 1 to 3 */
   int axis_pairs[3];       /* pairs of each axis, in order; they add up to rot_dim / 2 */
   float mscale;            /* factor on cos and sin (1 unless the scaling asks for one); finite */
-  const double* inv_freq;  /* device fp64 [rot_dim / 2]: radians a position */
+  const double* inv_freq;  /* device fp64 [rot_dim / 2]: radians a position; finite, angles below 2^50 */
 } hsa_rope_t;
 
 /* One tensor of token rows [T, H, d] inside a larger one: element (t, h, c) is at
@@ -518,11 +518,12 @@ hsa_status_t hkv_gather_quant(const hkv_quant_t* q, const void* const* page_k, c
  * h / (Hq / H).  Keys are used as stored (rotate them as they are written).  Q:
  * [T, Hq, d] bf16, Hq a multiple of H; out: [T, Hq, d] fp32, or bf16 when out_is_bf16;
  * lse (optional): [T, Hq] fp32.  scale: 0 means 1/sqrt(d).  Scores beyond fp32's range
- * give NaN.  Weights are fp32; softmax weight x value scale enters the products with an error
- * below 2^-22 of its own, or 2^-51 of the largest one of its head, query and group among 32 rows,
- * and an element of Q with one below 2^-25 of its query's largest.  n = 0 gives o = 0 and lse = -inf; a bad page sets HSA_ERR_DEVICE and its rows
- * are not attended to.  Two results over disjoint rows merge by their lse.  T <= 64; for a whole chunk assemble the cache
- * and use hsa_forward.  T may be 0.  Deterministic.  Workspace:
+ * give NaN; the sums of weights (at most 64 a row) times values are fp32 too and are to stay within
+ * its range.  A softmax weight times its value scale enters the products with an error below 2^-22
+ * of its own, or 2^-51 of the largest one of its head, query and group among 32 rows; an element
+ * of Q with one below 2^-25 of its query's largest.  n = 0 gives o = 0 and lse = -inf; a bad page
+ * sets HSA_ERR_DEVICE and its rows are not attended to.  Two results over disjoint rows merge by
+ * their lse.  T <= 64; for a whole chunk assemble the cache and use hsa_forward.  T may be 0.  Deterministic.  Workspace:
  * hkv_attn_quant_workspace_size() bytes, its 256-byte header as every workspace's. */
 hsa_status_t hkv_attn_quant_workspace_size(int T, int Hq, int H, int d, int Kp, int P_tok, size_t* bytes);
 hsa_status_t hkv_attn_quant(const hkv_quant_t* q, const hsa_bf16* Q, int T, int Hq, const void* const* page_k,
